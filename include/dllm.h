@@ -504,6 +504,101 @@ dllm_status dllm_attention_bf16_noalloc(const void* q, const void* k_cache, cons
                                         dllm_stream_t stream);
 
 /*
+ * The 8-bit K/V cache.  A layer's K and V are e4m3 codes [B, N, n_kv_heads,
+ * head_dim] (one byte each) and float scales [B, n_kv_heads, ceil(N/block)],
+ * one per sequence, head and block of `block` consecutive positions (16, 32,
+ * 64 or 128); a code c stands for c * scale.  Scales are powers of two not
+ * below 2^-100, so a decoded value is exact in bf16.  Codes and scales start
+ * as zeros: a block whose scale is below 2^-100 holds no rows.
+ *
+ * Rows of the calls below: sequence b has count[b] rows (count NULL: k_cap)
+ * at positions idx[b*k_cap + j], strictly ascending (idx NULL: position j);
+ * compact tensors hold them packed by sequence as in dllm_partial_layer, row
+ * r starting at element r * ld.  ws: NULL, or 256 bytes (256-byte aligned)
+ * whose device status word receives DLLM_DEV_CAPACITY for a count outside
+ * [0, k_cap] (clamped) and DLLM_DEV_BAD_INDEX for a list that is not strictly
+ * ascending within [0, N): rows at positions outside are skipped, which of
+ * the rows with the same position counts is unspecified.  B * k_cap <= 2^30.
+ */
+
+/* dllm_rope_table - cos and sin of position p and pair j, angle p *
+ * theta^(-2j/head_dim) computed in double: table [N, head_dim/2, 2] f32. */
+dllm_status dllm_rope_table(float* table, int N, int head_dim, float theta, dllm_stream_t stream);
+
+/*
+ * dllm_qk_norm_rope - RMS norm of every query and key head and the rotation of
+ * its position, in one pass: y = x / sqrt(mean(x^2) + eps) * gain over each
+ * head's head_dim elements, then the rotate-half pairs (j, j + head_dim/2) by
+ * the angles of rope (a dllm_rope_table of at least N positions; NULL: none).
+ * fp32 inside, rounded once when stored.
+ * q, q_out: compact rows of n_heads*head_dim (strides ldq, ldqo); k, k_out:
+ * compact rows of n_kv_heads*head_dim (ldk, ldko), or, with k_in_is_cache /
+ * k_out_is_cache, the rows at their positions of a cache [B, N, n_kv_heads,
+ * head_dim] (the stride is ignored).  q_gain, k_gain [head_dim].  An output
+ * may be its input (same pointer, stride and kind), and may not overlap it
+ * otherwise.  DLLM_BF16: head_dim 64 or 128, strides multiples of 8;
+ * DLLM_F32: even head_dim <= 256.  Pointers 16-byte aligned (DLLM_F32 rows and
+ * gains: 4).
+ */
+dllm_status dllm_qk_norm_rope(const void* q, int ldq, const void* k, int ldk, int k_in_is_cache,
+                              const void* q_gain, const void* k_gain, const float* rope,
+                              void* q_out, int ldqo, void* k_out, int ldko, int k_out_is_cache,
+                              const int32_t* idx, const int32_t* count, int k_cap, int B, int N,
+                              int n_heads, int n_kv_heads, int head_dim, float eps, int dtype,
+                              void* ws, size_t ws_bytes, dllm_stream_t stream);
+
+/* floats in each of k_scale and v_scale; 0 for bad arguments */
+size_t dllm_kv8_scale_count(int B, int N, int n_kv_heads, int block);
+
+/*
+ * dllm_kv8_write - bf16 K and V rows into the 8-bit cache.  For each block of
+ * positions with new rows, and each head, K and V apart: a = the largest
+ * finite magnitude among its new rows;
+ *   the scale stays   if some position of the block is not written by this
+ *                     call, the scale is at least 2^-100 and a <= 448 scale;
+ *   otherwise it is   the smallest power of two s >= 2^-100 with a <= 448 s.
+ * New rows are stored as x / s rounded to nearest even, NaN and infinities as
+ * NaN.  Where the scale changed, the block's other positions are re-encoded at
+ * it (exactly, but for bits below e4m3's smallest step 2^-9), or zeroed if
+ * the block held no rows.  Blocks without new rows are untouched; a call that
+ * is repeated changes nothing.  k, v: compact rows of n_kv_heads*head_dim
+ * bf16, strides multiples of 8, 16-byte aligned; head_dim 64 or 128.
+ */
+dllm_status dllm_kv8_write(const void* k, int ldk, const void* v, int ldv, const int32_t* idx,
+                           const int32_t* count, int k_cap, int B, int N, int n_kv_heads,
+                           int head_dim, int block, void* k8, float* k_scale, void* v8,
+                           float* v_scale, void* ws, size_t ws_bytes, dllm_stream_t stream);
+
+/* dllm_kv8_read - rows of the cache back to compact bf16 rows (exact); strides
+ * and alignment as for dllm_kv8_write. */
+dllm_status dllm_kv8_read(const void* k8, const float* k_scale, const void* v8,
+                          const float* v_scale, const int32_t* idx, const int32_t* count,
+                          int k_cap, int B, int N, int n_kv_heads, int head_dim, int block,
+                          void* k_out, int ldk, void* v_out, int ldv, void* ws, size_t ws_bytes,
+                          dllm_stream_t stream);
+
+/*
+ * dllm_attention_kv8 - dllm_attention_bf16 over the 8-bit cache: the compact
+ * query rows of sequence b (count[b] of them; count NULL: k_cap) attend to
+ * the first kv_len[b] cached positions (NULL: all N; a length outside [0, N]
+ * is clamped and sets DLLM_DEV_BAD_SHAPE).  Rows of a sequence without keys
+ * get zeros.  What the cache holds past kv_len[b] plays no part.  q, o: compact
+ * [B*k_cap, n_heads*head_dim] bf16, rows behind the last sequence's untouched.
+ * m, l: both NULL, or [B*k_cap, n_heads] f32 softmax statistics as
+ * dllm_attention_stats_bf16 returns them, here with 1 <= l < 2 (-inf and 0
+ * without keys).  Any N.
+ * ws: dllm_attention_kv8_workspace_size() bytes; calls that may overlap need a
+ * workspace each.
+ */
+size_t dllm_attention_kv8_workspace_size(int B, int k_cap, int N, int n_heads, int n_kv_heads,
+                                         int head_dim);
+dllm_status dllm_attention_kv8(const void* q, const void* k8, const float* k_scale,
+                               const void* v8, const float* v_scale, void* o, float* m, float* l,
+                               const int32_t* count, const int32_t* kv_len, int B, int k_cap,
+                               int N, int n_heads, int n_kv_heads, int head_dim, int block,
+                               void* ws, size_t ws_bytes, dllm_stream_t stream);
+
+/*
  * dllm_get_device_status - synchronises `stream`, copies the device status
  * word of a workspace used by dllm_select / dllm_partial_layer / dllm_step
  * into *status_out (HOST memory), and clears it.  Returns DLLM_ERR_DEVICE

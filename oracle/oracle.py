@@ -199,6 +199,8 @@ class LayerW:
     w_gate: np.ndarray      # [F, d]
     w_up: np.ndarray        # [F, d]
     w_down: np.ndarray      # [d, F]
+    q_norm: Optional[np.ndarray] = None  # [hd] gains of the per-head q/k norm (both or none)
+    k_norm: Optional[np.ndarray] = None
 
 
 @dataclass
@@ -229,6 +231,7 @@ class Policy:
     unmask_tau: float = 0.0       # > 0: over-threshold unmasking with top-n fallback
     refresh_every: int = 0        # generation: dense step every R steps (0: never)
     refresh_on_block: bool = False  # generation: dense step when a block changes
+    kv8_block: int = 0            # K/V caches in 8 bits, a scale per block of so many positions
 
 
 @dataclass
@@ -248,6 +251,9 @@ class State:
     q: Optional[List[np.ndarray]] = None
     att_m: Optional[List[np.ndarray]] = None
     att_l: Optional[List[np.ndarray]] = None
+    # 8-bit caches: k/v hold the decoded values; per layer the scales [B, Hkv, blocks]
+    k_scale: Optional[List[np.ndarray]] = None
+    v_scale: Optional[List[np.ndarray]] = None
 
     def copy(self) -> "State":
         cp = lambda a: None if a is None else [x.copy() for x in a]
@@ -255,11 +261,14 @@ class State:
                      [a.copy() for a in self.v], self.h_ref.copy(),
                      self.conf.copy(), self.pred.copy(),
                      None if self.h_ref2 is None else self.h_ref2.copy(), cp(self.ctx),
-                     cp(self.ffn), cp(self.q), cp(self.att_m), cp(self.att_l))
+                     cp(self.ffn), cp(self.q), cp(self.att_m), cp(self.att_l), cp(self.k_scale),
+                     cp(self.v_scale))
 
 
-def empty_state(cfg: ModelCfg, tokens: np.ndarray) -> State:
+def empty_state(cfg: ModelCfg, tokens: np.ndarray, kv8_block: int = 0) -> State:
     B, N = tokens.shape
+    scales = lambda: ([np.zeros((B, cfg.n_kv_heads, -(-N // kv8_block)))
+                       for _ in range(cfg.n_layers)] if kv8_block else None)
     kv = (B, N, cfg.n_kv_heads, cfg.head_dim)
     return State(np.array(tokens, dtype=np.int64).copy(),
                  [np.zeros(kv) for _ in range(cfg.n_layers)],
@@ -270,7 +279,8 @@ def empty_state(cfg: ModelCfg, tokens: np.ndarray) -> State:
                  [np.zeros((B, N, cfg.d)) for _ in range(cfg.n_layers)],
                  [np.zeros((B, N, cfg.n_heads * cfg.head_dim)) for _ in range(cfg.n_layers)],
                  [np.zeros((B, N, cfg.n_heads)) for _ in range(cfg.n_layers)],
-                 [np.zeros((B, N, cfg.n_heads)) for _ in range(cfg.n_layers)])
+                 [np.zeros((B, N, cfg.n_heads)) for _ in range(cfg.n_layers)],
+                 scales(), scales())
 
 
 # ---------------------------------------------------------------------------
@@ -389,6 +399,60 @@ def attention_update(q, m, l, o, K_old, V_old, K_new, V_new):
     return m2, l2, o2
 
 
+# ---------------------------------------------------------------------------
+# 8-bit K/V cache
+# ---------------------------------------------------------------------------
+
+E4M3_MAX = 448.0
+KV8_MIN_SCALE = 2.0 ** -100
+
+
+def e4m3_round(x) -> np.ndarray:
+    """Nearest e4m3 value (ties to even) of |x| <= 448: 3 mantissa bits, smallest
+    step 2^-9 (below 2^-6).  NaN and infinities become NaN."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        _, e = np.frexp(x)                     # x = f 2^e, 0.5 <= |f| < 1
+        step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+        y = np.round(x / step) * step
+    return np.where(np.isfinite(x), y, np.nan)
+
+
+def kv8_scale(amax: float) -> float:
+    """Smallest power of two s >= 2^-100 with amax <= 448 s."""
+    s = KV8_MIN_SCALE
+    while amax > E4M3_MAX * s:
+        s *= 2.0
+    return s
+
+
+def kv8_write(cache: np.ndarray, scale: np.ndarray, x: np.ndarray, b_of: np.ndarray,
+              pos: np.ndarray, block: int) -> None:
+    """Rows x [R, H, hd] into a cache of decoded values [B, N, H, hd] with scales
+    [B, H, blocks], in place.  Per sequence, block with new rows and head: the scale
+    stays when a position is kept, it is at least 2^-100 and covers the largest finite
+    new magnitude (a <= 448 s); else it is kv8_scale(a), and the kept positions are
+    rounded again at it (zeros when the block held no rows)."""
+    B, N, H, _ = cache.shape
+    for b in range(B):
+        mine = np.nonzero(b_of == b)[0]
+        for blk in np.unique(pos[mine] // block):
+            r = mine[pos[mine] // block == blk]
+            p0, p1 = blk * block, min((blk + 1) * block, N)
+            kept = np.setdiff1d(np.arange(p0, p1), pos[r])
+            for h in range(H):
+                y = x[r, h]
+                a = float(np.max(np.where(np.isfinite(y), np.abs(y), 0.0)))
+                s0 = scale[b, h, blk]
+                s = s0
+                if len(kept) == 0 or not s0 >= KV8_MIN_SCALE or a > E4M3_MAX * s0:
+                    s = kv8_scale(a)
+                    old = cache[b, kept, h] if s0 >= KV8_MIN_SCALE else 0.0 * cache[b, kept, h]
+                    cache[b, kept, h] = e4m3_round(old / s) * s
+                cache[b, pos[r], h] = e4m3_round(y / s) * s
+                scale[b, h, blk] = s
+
+
 def silu(x: np.ndarray) -> np.ndarray:
     return x / (1.0 + np.exp(-x))
 
@@ -412,8 +476,9 @@ class FfnGate:
 
 def layer_rows(cfg: ModelCfg, w: LayerW, x: np.ndarray, b_of_row: np.ndarray,
                pos_of_row: np.ndarray, k_cache: np.ndarray, v_cache: np.ndarray,
-               gate: Optional[FfnGate] = None) -> np.ndarray:
+               gate: Optional[FfnGate] = None, kv8=None) -> np.ndarray:
     """One transformer layer on a set of rows; updates the layer's K/V cache.
+    kv8: (k scales, v scales, block) of a cache held in 8 bits, or None.
 
     ``x`` [R, d] are the rows' layer inputs; row r belongs to sequence
     ``b_of_row[r]`` at position ``pos_of_row[r]``.  The rows' new K/V
@@ -425,15 +490,25 @@ def layer_rows(cfg: ModelCfg, w: LayerW, x: np.ndarray, b_of_row: np.ndarray,
     Hq, Hkv, hd = cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
     R = x.shape[0]
     n = store(rms_norm(x, w.attn_norm, cfg.rms_eps), dt)
-    q = rope((n @ w.wq.T).reshape(R, Hq, hd), pos_of_row, cfg.rope_theta)
-    k = rope((n @ w.wk.T).reshape(R, Hkv, hd), pos_of_row, cfg.rope_theta)
+    q, k = (n @ w.wq.T).reshape(R, Hq, hd), (n @ w.wk.T).reshape(R, Hkv, hd)
+    if w.q_norm is not None:
+        # the projections are stored before the per-head norm reads them
+        q = rms_norm(store(q, dt), w.q_norm, cfg.rms_eps)
+        k = rms_norm(store(k, dt), w.k_norm, cfg.rms_eps)
+    q = rope(q, pos_of_row, cfg.rope_theta)
+    k = rope(k, pos_of_row, cfg.rope_theta)
     v = (n @ w.wv.T).reshape(R, Hkv, hd)
     q, k, v = store(q, dt), store(k, dt), store(v, dt)
     upd = gate is not None and gate.q is not None
-    if upd:
+    if upd:  # (of a cache in 8 bits: its decoded values)
         k_old, v_old = k_cache[b_of_row, pos_of_row], v_cache[b_of_row, pos_of_row]
-    k_cache[b_of_row, pos_of_row] = k
-    v_cache[b_of_row, pos_of_row] = v
+    if kv8 is not None:
+        kv8_write(k_cache, kv8[0], k, b_of_row, pos_of_row, kv8[2])
+        kv8_write(v_cache, kv8[1], v, b_of_row, pos_of_row, kv8[2])
+        k, v = k_cache[b_of_row, pos_of_row], v_cache[b_of_row, pos_of_row]
+    else:
+        k_cache[b_of_row, pos_of_row] = k
+        v_cache[b_of_row, pos_of_row] = v
     o = np.empty((R, Hq, hd))
     for b in np.unique(b_of_row):
         rows = np.nonzero(b_of_row == b)[0]
@@ -666,8 +741,12 @@ def embed(W: ModelW, tokens: np.ndarray) -> np.ndarray:
     return np.asarray(W.embed, dtype=np.float64)[tokens]
 
 
+def _kv8_of(st: State, block: int, l: int):
+    return (st.k_scale[l], st.v_scale[l], block) if block else None
+
+
 def dense_layers(cfg: ModelCfg, W: ModelW, st: State, h: np.ndarray, upto: int,
-                 gate_on: bool = False) -> np.ndarray:
+                 gate_on: bool = False, kv8_block: int = 0) -> np.ndarray:
     """Layers 0 .. upto-1 on every row (writes every row's K/V there)."""
     B, N, d = h.shape
     b_of = np.repeat(np.arange(B), N)
@@ -675,7 +754,8 @@ def dense_layers(cfg: ModelCfg, W: ModelW, st: State, h: np.ndarray, upto: int,
     x = h.reshape(B * N, d)
     for l in range(upto):
         gate = FfnGate(st.ctx[l], st.ffn[l], 0.0, True) if gate_on else None
-        x = layer_rows(cfg, W.layers[l], x, b_of, p_of, st.k[l], st.v[l], gate)
+        x = layer_rows(cfg, W.layers[l], x, b_of, p_of, st.k[l], st.v[l], gate,
+                       _kv8_of(st, kv8_block, l))
     return x.reshape(B, N, d)
 
 
@@ -719,7 +799,7 @@ def step(cfg: ModelCfg, W: ModelW, st: State, pol: Policy, dense: bool,
     ls = pol.score_layer
     masked = st.tokens == cfg.mask_id
     h = embed(W, st.tokens)
-    h = dense_layers(cfg, W, st, h, ls, pol.ffn_gate)
+    h = dense_layers(cfg, W, st, h, ls, pol.ffn_gate, pol.kv8_block)
     scores = None
     if dense:
         idx = [np.arange(N, dtype=np.int64) for _ in range(B)]
@@ -748,7 +828,8 @@ def step(cfg: ModelCfg, W: ModelW, st: State, pol: Policy, dense: bool,
             gate = FfnGate(st.ctx[l], st.ffn[l], pol.ffn_tau, dense) if pol.ffn_gate else None
             if gate is not None and pol.attn_update:
                 gate.q, gate.att_m, gate.att_l = st.q[l], st.att_m[l], st.att_l[l]
-            x = layer_rows(cfg, W.layers[l], x, b_of, p_of, st.k[l], st.v[l], gate)
+            x = layer_rows(cfg, W.layers[l], x, b_of, p_of, st.k[l], st.v[l], gate,
+                           _kv8_of(st, pol.kv8_block, l))
             if gate is not None:
                 ffn_rows.append(int(np.sum(gate.salient)))
                 ffn_sal.append(gate.salient.copy())

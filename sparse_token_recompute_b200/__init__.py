@@ -127,6 +127,17 @@ _attn_upd = _sig("dllm_attention_update_bf16", _i, [vp, vp, vp, vp, vp, _i, _i, 
                                                     vp, _i, _i, _i, _i, vp, _sz, vp])
 _attn = _sig("dllm_attention_bf16", _i, [vp, vp, vp, vp, vp, _i, _i, _i, _i, _i, _i, vp, _sz,
                                          vp])
+_rope_table = _sig("dllm_rope_table", _i, [vp, _i, _i, _f, vp])
+_qk_norm = _sig("dllm_qk_norm_rope", _i, [vp, _i, vp, _i, _i, vp, vp, vp, vp, _i, vp, _i, _i, vp,
+                                          vp, _i, _i, _i, _i, _i, _i, _f, _i, vp, _sz, vp])
+_kv8_scales = _sig("dllm_kv8_scale_count", _sz, [_i, _i, _i, _i])
+_kv8_write = _sig("dllm_kv8_write", _i, [vp, _i, vp, _i, vp, vp, _i, _i, _i, _i, _i, _i, vp, vp,
+                                         vp, vp, vp, _sz, vp])
+_kv8_read = _sig("dllm_kv8_read", _i, [vp, vp, vp, vp, vp, vp, _i, _i, _i, _i, _i, _i, vp, _i,
+                                       vp, _i, vp, _sz, vp])
+_attn_kv8_ws = _sig("dllm_attention_kv8_workspace_size", _sz, [_i, _i, _i, _i, _i, _i])
+_attn_kv8 = _sig("dllm_attention_kv8", _i, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, _i, _i, _i,
+                                            _i, _i, _i, _i, vp, _sz, vp])
 _gemm_ws = _sig("dllm_gemm_workspace_size", _sz, [_i, _i, _i, _i])
 _gemm = _sig("dllm_gemm_bf16", _i, [vp, vp, vp, _i, _i, _i, _i, _i, vp, _sz, vp])
 _gemm_stall = _sig("dllm_selftest_gemm_stall", _i, [vp, vp, vp, _i, _i, _i, vp, _sz, vp])
@@ -378,6 +389,203 @@ def dllm_attention_bf16_noalloc(q, k_cache, v_cache, o, count, k_cap: int, strea
     _check(st, "dllm_attention_bf16_noalloc")
 
 
+# ----------------------------------------------------------------- 8-bit K/V cache
+
+def _want(name: str, t, dtype, device, shape=None, rows_of=None):
+    """Refuses a tensor that the library would misread: another type or device, other sizes
+    (None: any), or rows that are not contiguous (rows_of: a 2-D tensor's row length)."""
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{name}: dtype {t.dtype}, wanted {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, wanted {device}")
+    if rows_of is not None:
+        if t.dim() != 2 or t.shape[1] != rows_of or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, wanted rows "
+                             f"of {rows_of} contiguous elements")
+        if t.shape[0] > 1 and t.stride(0) < rows_of:
+            raise ValueError(f"{name}: rows overlap (stride {t.stride(0)})")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if shape is not None and (t.dim() != len(shape) or any(
+            w is not None and w != h for w, h in zip(shape, t.shape))):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+
+
+def _ld(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _on(device):
+    """The device made current for a call (nothing to do when it is)."""
+    import contextlib
+    import torch
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _row_lists(idx, count, device, B, rows: int, least: int = 1):
+    """(k_cap) of idx [B, k_cap] / count [B] over compact tensors of `rows` rows."""
+    import torch
+    if idx is not None:
+        _want("idx", idx, torch.int32, device, (B, None))
+        k_cap = idx.shape[1]
+    else:
+        k_cap = rows // B if B else 0
+    if count is not None:
+        _want("count", count, torch.int32, device, (B,))
+    if rows < B * k_cap or (B and k_cap < least):
+        raise ValueError(f"compact tensors of {rows} rows for {B} sequences of {k_cap}")
+    return k_cap
+
+
+def dllm_rope_table(table, theta: float, stream=None):
+    """table [N, head_dim/2, 2] float32 <- cos, sin of the rotation angles."""
+    import torch
+    _want("table", table, torch.float32, table.device, (None, None, 2))
+    with _on(table.device):
+        st = _rope_table(ptr(table), table.shape[0], 2 * table.shape[1], float(theta),
+                         _stream(stream))
+    _check(st, "dllm_rope_table")
+
+
+def dllm_qk_norm_rope(q, k, q_gain, k_gain, rope, q_out, k_out, idx, count, eps: float,
+                      N: int = None, ws: Workspace = None, stream=None):
+    """Per-head RMS norm of q and k rows and their rotation (see include/dllm.h).  q, q_out:
+    [rows, n_heads*head_dim]; k, k_out: [rows, n_kv_heads*head_dim] compact rows, or a
+    [B, N, n_kv_heads, head_dim] cache whose rows at the positions are meant; rope: a
+    dllm_rope_table or None; idx [B, k_cap] and count [B] as for dllm_partial_layer.  The
+    number of positions N comes from a cache or the table."""
+    import torch
+    dev, dt = q.device, q.dtype
+    hd = q_gain.shape[0]
+    code = _dtype_code(q)
+    if idx is None and count is None:
+        raise ValueError("idx or count: the number of sequences is theirs")
+    B = (idx if idx is not None else count).shape[0]
+    caches = [t.shape[1] for t in (k, k_out) if t.dim() == 4]
+    if N is None:
+        N = caches[0] if caches else rope.shape[0]
+    wq = q.shape[1]
+    wk = k.shape[2] * hd if k.dim() == 4 else k.shape[1]
+    for name, t, w in (("q", q, wq), ("q_out", q_out, wq), ("k", k, wk), ("k_out", k_out, wk)):
+        if t.dim() == 4:
+            _want(name, t, dt, dev, (B, N, wk // hd, hd))
+        else:
+            _want(name, t, dt, dev, rows_of=w)
+    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
+        _want(name, t, dt, dev, (hd,))
+    if rope is not None:
+        _want("rope", rope, torch.float32, dev, (None, hd // 2, 2))
+        if rope.shape[0] < N:
+            raise ValueError(f"rope: {rope.shape[0]} positions, wanted {N}")
+    if wq % hd or wk % hd:
+        raise ValueError(f"rows of {wq} and {wk} elements for heads of {hd}")
+    k_cap = _row_lists(idx, count, dev, B, min(t.shape[0] for t in (q, q_out, k, k_out)
+                                               if t.dim() == 2))
+    with _on(dev):
+        st = _qk_norm(ptr(q), _ld(q), ptr(k), 0 if k.dim() == 4 else _ld(k), int(k.dim() == 4),
+                      ptr(q_gain), ptr(k_gain), ptr(rope), ptr(q_out), _ld(q_out), ptr(k_out),
+                      0 if k_out.dim() == 4 else _ld(k_out), int(k_out.dim() == 4), ptr(idx),
+                      ptr(count), k_cap, B, N, wq // hd, wk // hd, hd, float(eps), code,
+                      ws.ptr if ws else None, ws.nbytes if ws else 0, _stream(stream))
+    _check(st, "dllm_qk_norm_rope")
+
+
+def dllm_kv8_scale_count(B: int, N: int, n_kv_heads: int, block: int) -> int:
+    return int(_kv8_scales(B, N, n_kv_heads, block))
+
+
+def _kv8_cache(k8, k_scale, v8, v_scale, block: int):
+    import torch
+    B, N, H, hd = k8.shape
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    nblk = -(-N // block) if block > 0 else 0
+    for name, t in (("k8", k8), ("v8", v8)):
+        _want(name, t, codes, k8.device, (B, N, H, hd))
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _want(name, t, torch.float32, k8.device, (B, H, nblk))
+    return B, N, H, hd
+
+
+def kv8_cache(B: int, N: int, n_kv_heads: int, head_dim: int, block: int, device="cuda"):
+    """An empty 8-bit cache: codes [B, N, n_kv_heads, head_dim] (float8_e4m3fn) and scales
+    [B, n_kv_heads, ceil(N/block)] of zeros, as (k8, k_scale, v8, v_scale)."""
+    import torch
+    code = lambda: torch.zeros(B, N, n_kv_heads, head_dim, dtype=torch.uint8,
+                               device=device).view(torch.float8_e4m3fn)
+    scale = lambda: torch.zeros(B, n_kv_heads, -(-N // block), device=device)
+    return code(), scale(), code(), scale()
+
+
+def dllm_kv8_write(k, v, idx, count, k8, k_scale, v8, v_scale, block: int, ws: Workspace = None,
+                   stream=None):
+    """K/V rows [rows, n_kv_heads*head_dim] bf16 into the 8-bit cache at the positions idx
+    [B, k_cap] (None: row j at position j), count [B] of them (None: all)."""
+    import torch
+    B, N, H, hd = _kv8_cache(k8, k_scale, v8, v_scale, block)
+    for name, t in (("k", k), ("v", v)):
+        _want(name, t, torch.bfloat16, k8.device, rows_of=H * hd)
+    k_cap = _row_lists(idx, count, k8.device, B, min(k.shape[0], v.shape[0]))
+    with _on(k8.device):
+        st = _kv8_write(ptr(k), _ld(k), ptr(v), _ld(v), ptr(idx), ptr(count), k_cap, B, N, H, hd,
+                        int(block), ptr(k8), ptr(k_scale), ptr(v8), ptr(v_scale),
+                        ws.ptr if ws else None, ws.nbytes if ws else 0, _stream(stream))
+    _check(st, "dllm_kv8_write")
+
+
+def dllm_kv8_read(k8, k_scale, v8, v_scale, idx, count, k_out, v_out, block: int,
+                  ws: Workspace = None, stream=None):
+    """Rows of the 8-bit cache as bf16 compact rows [rows, n_kv_heads*head_dim]."""
+    import torch
+    B, N, H, hd = _kv8_cache(k8, k_scale, v8, v_scale, block)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _want(name, t, torch.bfloat16, k8.device, rows_of=H * hd)
+    k_cap = _row_lists(idx, count, k8.device, B, min(k_out.shape[0], v_out.shape[0]))
+    with _on(k8.device):
+        st = _kv8_read(ptr(k8), ptr(k_scale), ptr(v8), ptr(v_scale), ptr(idx), ptr(count), k_cap,
+                       B, N, H, hd, int(block), ptr(k_out), _ld(k_out), ptr(v_out), _ld(v_out),
+                       ws.ptr if ws else None, ws.nbytes if ws else 0, _stream(stream))
+    _check(st, "dllm_kv8_read")
+
+
+def dllm_attention_kv8_workspace_size(B, k_cap, N, n_heads, n_kv_heads, head_dim) -> int:
+    return int(_attn_kv8_ws(B, k_cap, N, n_heads, n_kv_heads, head_dim))
+
+
+def dllm_attention_kv8(q, k8, k_scale, v8, v_scale, o, count, k_cap: int, block: int, kv_len=None,
+                       m=None, l=None, ws: Workspace = None, stream=None):
+    """Attention of compact query rows [B*k_cap, n_heads*head_dim] over the 8-bit cache (the
+    first kv_len[b] positions of each sequence); returns the workspace, to be kept for the
+    next call of these sizes."""
+    import torch
+    B, N, H, hd = _kv8_cache(k8, k_scale, v8, v_scale, block)
+    dev = k8.device
+    wq = q.shape[1]
+    for name, t in (("q", q), ("o", o)):
+        _want(name, t, torch.bfloat16, dev, (None, wq))
+        if t.shape[0] < B * k_cap:
+            raise ValueError(f"{name}: {t.shape[0]} rows for {B} sequences of {k_cap}")
+    if wq % hd:
+        raise ValueError(f"rows of {wq} elements for heads of {hd}")
+    for name, t in (("count", count), ("kv_len", kv_len)):
+        if t is not None:
+            _want(name, t, torch.int32, dev, (B,))
+    for name, t in (("m", m), ("l", l)):
+        if t is not None:
+            _want(name, t, torch.float32, dev, (None, wq // hd))
+            if t.shape[0] < B * k_cap:
+                raise ValueError(f"{name}: {t.shape[0]} rows for {B} sequences of {k_cap}")
+    if ws is None:
+        ws = Workspace(dllm_attention_kv8_workspace_size(B, k_cap, N, wq // hd, H, hd), dev)
+    with _on(dev):
+        st = _attn_kv8(ptr(q), ptr(k8), ptr(k_scale), ptr(v8), ptr(v_scale), ptr(o), ptr(m),
+                       ptr(l), ptr(count), ptr(kv_len), B, int(k_cap), N, wq // hd, H, hd,
+                       int(block), ws.ptr, ws.nbytes, _stream(stream))
+    _check(st, "dllm_attention_kv8")
+    return ws
+
+
 def profile_enable(on: bool = True):
     _prof_enable(int(bool(on)))
 
@@ -589,6 +797,6 @@ class StepGraph:
 
 __all__ = [n for n in dir() if n.startswith(("dllm_", "DLLM_"))] + ["StepGraph",
 
-    "Model", "Cache", "Workspace", "ModelCfg", "LayerW", "Policy", "make_cfg", "cfg_from_shape",
+    "kv8_cache", "Model", "Cache", "Workspace", "ModelCfg", "LayerW", "Policy", "make_cfg", "cfg_from_shape",
     "make_policy", "profile_enable", "profile_reset", "profile_read", "status_string", "version",
     "DllmError", "LIB_PATH"]

@@ -178,6 +178,49 @@ cudaError_t launch_attention_update(const __nv_bfloat16* q, int R_cap, __nv_bflo
                                     const int* a_off, int A_cap, int B, int Hq, int Hkv, int hd,
                                     int* status, cudaStream_t s, const uint8_t* skip = nullptr);
 
+// ----- q/k norm and the 8-bit K/V cache -----
+// The rows of a call: idx/count/k_cap as the C entry points take them, or the row maps
+// that launch_row_map built (row_off non-null); M_cap bounds the compact rows.
+struct Kv8RowMap {
+  const int32_t* idx;
+  const int32_t* count;
+  const int* row_off;
+  const int* row_pos;
+  const int* row_seq;
+  int B, k_cap, N, M_cap;
+  int* status;
+};
+// per-head RMS norm of q (compact rows, stride ldq) and k (compact rows, or the cache rows
+// [B, N, Hkv, hd] when k_in_cache) and their rotation; k_out compact or the cache's rows.
+// In place where out == in.
+cudaError_t launch_qk_norm_rope(const Kv8RowMap& m, const void* q, size_t ldq, const void* k,
+                                size_t ldk, void* q_out, size_t ldqo, void* k_out, size_t ldko,
+                                const void* q_gain, const void* k_gain, const float2* rope, int Hq,
+                                int Hkv, int hd, float eps, bool bf16, bool k_in_cache,
+                                bool k_out_cache, cudaStream_t s);
+// e4m3 codes [B, N, Hkv, hd], scales [B, Hkv, ceil(N / block)], block 16/32/64/128
+cudaError_t launch_kv8_write(const Kv8RowMap& m, const __nv_bfloat16* k, size_t ldk,
+                             const __nv_bfloat16* v, size_t ldv, uint8_t* k8, float* ks,
+                             uint8_t* v8, float* vs, int Hkv, int hd, int block, cudaStream_t s);
+cudaError_t launch_kv8_read(const Kv8RowMap& m, const uint8_t* k8, const float* ks,
+                            const uint8_t* v8, const float* vs, __nv_bfloat16* k, size_t ldk,
+                            __nv_bfloat16* v, size_t ldv, int Hkv, int hd, int block,
+                            cudaStream_t s);
+struct Kv8AttnPlan {
+  int tiles, shares;  // tiles of packed query rows per (sequence, kv head); key shares
+  long long ctas;
+};
+Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd, size_t M_cap,
+                               size_t part_bytes);
+// scratch (fp32 partial outputs) of the plan for this shape
+size_t attention_kv8_part_bytes(int B, int k_cap, int N, int Hq, int Hkv, int hd);
+// kv_len null: every sequence has N keys; st_m/st_l [M_cap, Hq] may be null
+cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, const uint8_t* k8,
+                                 const float* ks, const uint8_t* v8, const float* vs,
+                                 __nv_bfloat16* o, const int* kv_len, int Hq, int Hkv, int hd,
+                                 int block, float* part, size_t part_bytes, float* st_m,
+                                 float* st_l, cudaStream_t s);
+
 // ----- score / select / unmask -----
 template <typename T>
 void launch_confidence(const T* logits, const int32_t* logit_pos, int B, int Mm, int V, int N,
