@@ -22,70 +22,11 @@
 // f16's range is kept however far apart the blocks' scales are.
 #include <algorithm>
 
-#include "internal.h"
-#include "kv8.cuh"
+#include "attention_kv8.cuh"
 
 namespace dllm {
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazy = 8.0f;  // how far below the largest x_j the reference may stay
-
-struct Kv8Args {
-  const __nv_bfloat16* q;
-  const uint8_t* k8;
-  const uint8_t* v8;
-  const float* ks;
-  const float* vs;
-  __nv_bfloat16* o;
-  const int* kv_len;  // null: N keys each
-  Kv8Rows rows;
-  int Hq, Hkv, G;
-  int nblk, blk_log2;
-  float scale_log2;  // log2(e) / sqrt(hd)
-  int tiles;         // tiles of packed rows per (sequence, kv head)
-  int S;             // key shares
-  int part_rows;
-  float* part_o;     // [S, part_rows, Hq, hd]
-  float* part_ml;    // [S, part_rows, Hq, 2]: reference maximum (log2 units), sum
-  float* st_m;       // softmax statistics (natural units), or null
-  float* st_l;
-};
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 t = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
-// 2^e, e clamped to normal floats
-__device__ __forceinline__ float pow2i(int e) {
-  return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
-}
-// log2 and inverse of a block's V scale; a block that holds no rows (its codes are zeros)
-// counts as scale 1
-__device__ __forceinline__ void v_scale_parts(float s, float& log2s, float& inv) {
-  const bool holds = s >= kKv8MinScale;
-  log2s = holds ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
-  inv = holds ? kv8_inverse(s) : 1.f;
-}
-// (m, l) with the same l 2^m and 1 <= l < 2; l = 0 stays, with m = -inf
-__device__ __forceinline__ void normal_stats(float& m, float& l) {
-  if (l == 0.f) m = -INFINITY;
-  if (!(l > 0.f) || l == INFINITY) return;
-  const uint32_t b = __float_as_uint(l);
-  m += (float)((int)(b >> 23) - 127);
-  l = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
-}
-// exponent that brings amax into [2^14, 2^15) (0 for a row of zeros)
-__device__ __forceinline__ int query_shift(float amax) {
-  const int e = (int)(__float_as_uint(amax) >> 23);
-  return e == 0 ? 0 : 14 + 127 - e;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
@@ -115,6 +56,8 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 
 // ---------------------------------------------------------------- few query rows
 
+// packed query rows per (sequence, kv head) that still run here
+constexpr int kKv8TcRows = 16;
 constexpr int RW = 4;        // warps per CTA
 constexpr int RM = 16;       // packed query rows per CTA
 constexpr int RK = 16;       // keys per warp and turn
@@ -299,7 +242,7 @@ __global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A)
       float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (mx > m[i] + kLazy) {
+      if (mx > m[i] + kKv8Lazy) {
         alpha[i] = exp2_approx(m[i] - mx);
         m[i] = mx;
         grew = true;
@@ -399,7 +342,7 @@ __global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A)
       *reinterpret_cast<uint4*>(A.o + at * HD + e) = pack8(acc);
       if (A.st_m && e == 0) {
         normal_stats(mx, sum);
-        A.st_m[at] = mx / kLog2e;
+        A.st_m[at] = mx / kKv8Log2e;
         A.st_l[at] = sum;
       }
     } else {
@@ -454,28 +397,9 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
     *reinterpret_cast<__nv_bfloat162*>(dst + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
   if (A.st_m && lane == 0) {
     normal_stats(mx, sum);
-    A.st_m[u] = mx / kLog2e;
+    A.st_m[u] = mx / kKv8Log2e;
     A.st_l[u] = sum;
   }
-}
-
-template <auto Kernel>
-cudaError_t launch(unsigned grid, unsigned threads, int smem, cudaStream_t s, const Kv8Args& A) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = ensure_smem_attr<Kernel>(smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute la[1];
-  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  la[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = la;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, Kernel, A);
 }
 
 size_t part_floats(int S, size_t rows, int Hq, int hd) {
@@ -488,11 +412,21 @@ Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd,
                                size_t part_bytes) {
   Kv8AttnPlan pl{};
   const long long packed = (long long)k_cap * (Hq / Hkv);
-  pl.tiles = (int)((packed + RM - 1) / RM);
+  const int keys = std::max(N, 1);
+  // resident CTAs per SM, and the keys that a share holds at least
+  int per_sm = 2, least = 256;
+  int rows = RM;
+  if (packed > kKv8TcRows) {
+    const long long tiles = (packed + 127) / 128;
+    pl.nt = tiles % 2 == 0 ? 2 : 1;
+    rows = 128 * pl.nt;
+    per_sm = pl.nt == 1 ? 2 : 1;
+    least = 128;
+  }
+  pl.tiles = (int)((packed + rows - 1) / rows);
   const long long units = (long long)B * Hkv * pl.tiles;
-  // two CTAs per SM; a share holds at least 256 keys
-  const long long want = std::max(1LL, 2LL * num_sms() / std::max(1LL, units));
-  pl.shares = (int)std::max(1LL, std::min({want, (long long)(N + 255) / 256, 64LL}));
+  const long long want = std::max(1LL, (long long)per_sm * num_sms() / std::max(1LL, units));
+  pl.shares = (int)std::max(1LL, std::min({want, (long long)(keys + least - 1) / least, 64LL}));
   while (pl.shares > 1 && part_floats(pl.shares, M_cap, Hq, hd) * sizeof(float) > part_bytes) --pl.shares;
   pl.ctas = units * pl.shares;
   return pl;
@@ -518,7 +452,7 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   A.Hq = Hq, A.Hkv = Hkv, A.G = Hq / Hkv;
   A.nblk = (m.N + block - 1) / block;
   while ((1 << A.blk_log2) < block) ++A.blk_log2;
-  A.scale_log2 = kLog2e / sqrtf((float)hd);
+  A.scale_log2 = kKv8Log2e / sqrtf((float)hd);
   A.tiles = pl.tiles;
   A.S = pl.shares;
   A.part_rows = m.M_cap;
@@ -528,14 +462,17 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   cudaError_t e;
   {
     ProfScope prof("attention_kv8", s);
-    e = hd == 128 ? launch<attn_kv8_rows_kernel<128>>((unsigned)pl.ctas, RW * 32, RowsSmem<128>::TOTAL, s, A)
-                  : launch<attn_kv8_rows_kernel<64>>((unsigned)pl.ctas, RW * 32, RowsSmem<64>::TOTAL, s, A);
+    if (pl.nt)
+      e = launch_attention_kv8_tc(A, pl.nt, pl.ctas, hd, s);
+    else
+      e = hd == 128 ? launch_kv8<attn_kv8_rows_kernel<128>>((unsigned)pl.ctas, RW * 32, RowsSmem<128>::TOTAL, s, A)
+                  : launch_kv8<attn_kv8_rows_kernel<64>>((unsigned)pl.ctas, RW * 32, RowsSmem<64>::TOTAL, s, A);
   }
   if (e != cudaSuccess || pl.shares == 1) return e;
   ProfScope prof("attention_kv8_merge", s);
   const unsigned grid = (unsigned)(((size_t)m.M_cap * Hq + 7) / 8);
-  return hd == 128 ? launch<attn_kv8_merge_kernel<128>>(grid, 256, 0, s, A)
-                   : launch<attn_kv8_merge_kernel<64>>(grid, 256, 0, s, A);
+  return hd == 128 ? launch_kv8<attn_kv8_merge_kernel<128>>(grid, 256, 0, s, A)
+                   : launch_kv8<attn_kv8_merge_kernel<64>>(grid, 256, 0, s, A);
 }
 
 }  // namespace dllm

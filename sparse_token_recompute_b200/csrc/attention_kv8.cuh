@@ -1,0 +1,91 @@
+// Shared by the two attention kernels over the 8-bit K/V cache: their arguments
+// and the arithmetic that attention_kv8.cu's head comment describes.
+#pragma once
+
+#include "internal.h"
+#include "kv8.cuh"
+
+namespace dllm {
+
+constexpr float kKv8Log2e = 1.4426950408889634f;
+constexpr float kKv8Lazy = 8.0f;  // how far below the largest x_j the reference may stay
+
+struct Kv8Args {
+  const __nv_bfloat16* q;
+  const uint8_t* k8;
+  const uint8_t* v8;
+  const float* ks;
+  const float* vs;
+  __nv_bfloat16* o;
+  const int* kv_len;  // null: N keys each
+  Kv8Rows rows;
+  int Hq, Hkv, G;
+  int nblk, blk_log2;
+  float scale_log2;  // log2(e) / sqrt(hd)
+  int tiles;         // CTAs' worth of packed rows per (sequence, kv head)
+  int S;             // key shares
+  int part_rows;
+  float* part_o;     // [S, part_rows, Hq, hd]
+  float* part_ml;    // [S, part_rows, Hq, 2]: reference maximum (log2 units), sum
+  float* st_m;       // softmax statistics (natural units), or null
+  float* st_l;
+};
+
+// 2^x, relative error about 2^-22; results below 2^-126 flush to zero
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 t = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+// 2^e, e clamped to normal floats
+__device__ __forceinline__ float pow2i(int e) {
+  return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
+}
+// log2 and inverse of a block's V scale; a block that holds no rows (its codes are zeros)
+// counts as scale 1
+__device__ __forceinline__ void v_scale_parts(float s, float& log2s, float& inv) {
+  const bool holds = s >= kKv8MinScale;
+  log2s = holds ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
+  inv = holds ? kv8_inverse(s) : 1.f;
+}
+// (m, l) with the same l 2^m and 1 <= l < 2; l = 0 stays, with m = -inf
+__device__ __forceinline__ void normal_stats(float& m, float& l) {
+  if (l == 0.f) m = -INFINITY;
+  if (!(l > 0.f) || l == INFINITY) return;
+  const uint32_t b = __float_as_uint(l);
+  m += (float)((int)(b >> 23) - 127);
+  l = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
+}
+// exponent that brings amax into [2^14, 2^15) (0 for a row of zeros)
+__device__ __forceinline__ int query_shift(float amax) {
+  const int e = (int)(__float_as_uint(amax) >> 23);
+  return e == 0 ? 0 : 14 + 127 - e;
+}
+
+// many packed rows: tiles of 128 on tcgen05, nt of them per CTA (attention_kv8_tc.cu)
+cudaError_t launch_attention_kv8_tc(const Kv8Args& A, int nt, long long ctas, int hd, cudaStream_t s);
+
+template <auto Kernel>
+cudaError_t launch_kv8(unsigned grid, unsigned threads, int smem, cudaStream_t s, const Kv8Args& A) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = ensure_smem_attr<Kernel>(smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = la;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, Kernel, A);
+}
+
+}  // namespace dllm

@@ -207,7 +207,8 @@ cudaError_t launch_kv8_read(const Kv8RowMap& m, const uint8_t* k8, const float* 
                             __nv_bfloat16* v, size_t ldv, int Hkv, int hd, int block,
                             cudaStream_t s);
 struct Kv8AttnPlan {
-  int tiles, shares;  // tiles of packed query rows per (sequence, kv head); key shares
+  int nt;             // 0: 16 packed query rows per CTA; 1, 2: so many tiles of 128
+  int tiles, shares;  // CTAs' worth of packed rows per (sequence, kv head); key shares
   long long ctas;
 };
 Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd, size_t M_cap,
