@@ -105,13 +105,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// max of three values in one instruction
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // barrier `id` over `count` threads (a multiple of 32) of the block
 __device__ __forceinline__ void named_bar_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
