@@ -396,19 +396,12 @@ Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd,
   Kv8AttnPlan pl{};
   const long long packed = (long long)k_cap * (Hq / Hkv);
   const int keys = std::max(N, 1);
-  // resident CTAs per SM, and the keys that a share holds at least
-  int per_sm = 2, least = 256;
-  int rows = RM;
-  if (packed > kKv8TcRows) {
-    const long long tiles = (packed + 127) / 128;
-    pl.nt = tiles % 2 == 0 ? 2 : 1;
-    rows = 128 * pl.nt;
-    per_sm = pl.nt == 1 ? 2 : 1;
-    least = 128;
-  }
+  pl.tc = packed > kKv8TcRows;
+  const int rows = pl.tc ? 128 : RM;
+  const int least = pl.tc ? 128 : 256;  // keys that a share holds at least
   pl.tiles = (int)((packed + rows - 1) / rows);
   const long long units = (long long)B * Hkv * pl.tiles;
-  const long long want = std::max(1LL, (long long)per_sm * num_sms() / std::max(1LL, units));
+  const long long want = std::max(1LL, 2LL * num_sms() / std::max(1LL, units));  // two CTAs per SM
   pl.shares = (int)std::max(1LL, std::min({want, (long long)(keys + least - 1) / least, 64LL}));
   while (pl.shares > 1 && part_floats(pl.shares, M_cap, Hq, hd) * sizeof(float) > part_bytes) --pl.shares;
   pl.ctas = units * pl.shares;
@@ -445,8 +438,8 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   cudaError_t e;
   {
     ProfScope prof("attention_kv8", s);
-    if (pl.nt)
-      e = launch_attention_kv8_tc(A, pl.nt, pl.ctas, hd, s);
+    if (pl.tc)
+      e = launch_attention_kv8_tc(A, pl.ctas, hd, s);
     else
       e = hd == 128 ? launch_kv8<attn_kv8_rows_kernel<128>>((unsigned)pl.ctas, RW * 32, RowsSmem<128>::TOTAL, s, A)
                   : launch_kv8<attn_kv8_rows_kernel<64>>((unsigned)pl.ctas, RW * 32, RowsSmem<64>::TOTAL, s, A);

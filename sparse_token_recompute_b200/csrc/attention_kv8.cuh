@@ -70,6 +70,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0)
                : "memory");
@@ -83,8 +86,8 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// many packed rows: tiles of 128 on tcgen05, nt of them per CTA (attention_kv8_tc.cu)
-cudaError_t launch_attention_kv8_tc(const Kv8Args& A, int nt, long long ctas, int hd, cudaStream_t s);
+// many packed rows: tiles of 128 on tcgen05 (attention_kv8_tc.cu)
+cudaError_t launch_attention_kv8_tc(const Kv8Args& A, long long ctas, int hd, cudaStream_t s);
 
 template <auto Kernel>
 cudaError_t launch_kv8(unsigned grid, unsigned threads, int smem, cudaStream_t s, const Kv8Args& A) {

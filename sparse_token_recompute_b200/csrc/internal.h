@@ -207,7 +207,7 @@ cudaError_t launch_kv8_read(const Kv8RowMap& m, const uint8_t* k8, const float* 
                             __nv_bfloat16* v, size_t ldv, int Hkv, int hd, int block,
                             cudaStream_t s);
 struct Kv8AttnPlan {
-  int nt;             // 0: 16 packed query rows per CTA; 1, 2: so many tiles of 128
+  bool tc;            // tiles of 128 packed query rows on tcgen05, else of 16
   int tiles, shares;  // CTAs' worth of packed rows per (sequence, kv head); key shares
   long long ctas;
 };
