@@ -17,6 +17,8 @@ import json
 import os
 from typing import Dict, List, Optional, Sequence
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdllm.so")
 
@@ -390,60 +392,110 @@ def dllm_attention_bf16_noalloc(q, k_cache, v_cache, o, count, k_cap: int, strea
 
 
 # ----------------------------------------------------------------- 8-bit K/V cache
+#
+# A call for a handful of rows costs the GPU a few microseconds, so the checks below are
+# written to cost little when they pass: each function compares what it needs at once and
+# looks for the reason only when something does not fit.
 
-def _want(name: str, t, dtype, device, shape=None, rows_of=None):
-    """Refuses a tensor that the library would misread: another type or device, other sizes
-    (None: any), or rows that are not contiguous (rows_of: a 2-D tensor's row length)."""
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise TypeError(f"{name}: dtype {t.dtype}, wanted {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, wanted {device}")
-    if rows_of is not None:
-        if t.dim() != 2 or t.shape[1] != rows_of or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, wanted rows "
-                             f"of {rows_of} contiguous elements")
-        if t.shape[0] > 1 and t.stride(0) < rows_of:
-            raise ValueError(f"{name}: rows overlap (stride {t.stride(0)})")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    if shape is not None and (t.dim() != len(shape) or any(
-            w is not None and w != h for w, h in zip(shape, t.shape))):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
-
-
-def _ld(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _on(device):
-    """The device made current for a call (nothing to do when it is)."""
-    import contextlib
-    import torch
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _bad(checks, device):
+    """Raises the error of the first failing check of [(name, tensor, dtypes, shape)]: shape
+    None entries are any size; ("rows", w) wants a 2-D tensor of w contiguous elements per
+    row."""
+    for name, t, dtypes, shape in checks:
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype}, wanted {' or '.join(map(str, dtypes))}")
+        if shape[0] == "rows":
+            if t.dim() != 2 or t.shape[1] != shape[1] or (shape[1] > 1 and t.stride(1) != 1) or (
+                    t.shape[0] > 1 and t.stride(0) < shape[1]):
+                raise ValueError(f"{name}: shape {tuple(t.shape)} strides {t.stride()}, wanted "
+                                 f"rows of {shape[1]} contiguous elements that do not overlap")
+        elif not t.is_contiguous():
+            raise ValueError(f"{name}: not contiguous")
+        elif len(shape) != t.dim() or any(w is not None and w != h for w, h in zip(shape, t.shape)):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {shape}")
+    for name, t, _, _ in checks:
+        if t is not None and (t.get_device() < 0 or t.get_device() != device):
+            raise ValueError(f"{name}: on {t.device}, wanted a CUDA tensor on the others' device")
+    raise ValueError("arguments that do not fit together")
 
 
-def _row_lists(idx, count, device, B, rows: int, least: int = 1):
-    """(k_cap) of idx [B, k_cap] / count [B] over compact tensors of `rows` rows."""
-    import torch
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+
+
+def _kv8_checks(k8, k_scale, v8, v_scale, B, N, H, hd, nblk):
+    f32 = (_F32,)
+    return [("k8", k8, _CODES, (B, N, H, hd)), ("v8", v8, _CODES, (B, N, H, hd)),
+            ("k_scale", k_scale, f32, (B, H, nblk)), ("v_scale", v_scale, f32, (B, H, nblk))]
+
+
+def _cache_fits(k8, ks, v8, vs, shape, scales, dev):
+    return (k8.dtype in _CODES and v8.dtype in _CODES and ks.dtype is _F32 and vs.dtype is _F32
+            and v8.shape == shape and ks.shape == scales and vs.shape == scales
+            and k8.is_contiguous() and v8.is_contiguous() and ks.is_contiguous()
+            and vs.is_contiguous() and dev >= 0 and v8.get_device() == dev
+            and ks.get_device() == dev and vs.get_device() == dev)
+
+
+def _rows_fit(t, dtype, width, dev):
+    """The row stride of a 2-D tensor of `width` contiguous elements per row, 0 if it is none."""
+    sh = t.shape
+    if t.dtype is not dtype or len(sh) != 2 or sh[1] != width or t.get_device() != dev:
+        return 0
+    if sh[0] <= 1 and t.is_contiguous():
+        return width
+    a, b = t.stride()
+    return a if (b == 1 or width == 1) and a >= width else 0
+
+
+def _lists_fit(idx, count, B, rows, dev):
+    """k_cap of idx [B, k_cap] / count [B] over compact tensors of `rows` rows; 0 if they do
+    not fit."""
+    k_cap = rows // B if B else 1
     if idx is not None:
-        _want("idx", idx, torch.int32, device, (B, None))
-        k_cap = idx.shape[1]
+        sh = idx.shape
+        if len(sh) != 2 or sh[0] != B or idx.dtype is not _I32 or not idx.is_contiguous() or (
+                idx.get_device() != dev):
+            return 0
+        k_cap = sh[1]
+    if count is not None and (count.shape != (B,) or count.dtype is not _I32
+                              or not count.is_contiguous() or count.get_device() != dev):
+        return 0
+    return k_cap if rows >= B * k_cap else 0
+
+
+def _list_checks(idx, count, B):
+    i32 = (_I32,)
+    return [("idx", idx, i32, (B, None)), ("count", count, i32, (B,))]
+
+
+def _launch(dev: int, fn, args, ws, stream, where: str):
+    """fn(*args, workspace, bytes, stream) on device `dev`, which is made current for the call."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    p, n = (None, 0) if ws is None else (ws.buf.data_ptr(), ws.nbytes)
+    if ws is not None and ws.buf.get_device() != dev:
+        raise ValueError(f"{where}: the workspace is on {ws.buf.device}")
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, p, n, stream)
     else:
-        k_cap = rows // B if B else 0
-    if count is not None:
-        _want("count", count, torch.int32, device, (B,))
-    if rows < B * k_cap or (B and k_cap < least):
-        raise ValueError(f"compact tensors of {rows} rows for {B} sequences of {k_cap}")
-    return k_cap
+        with torch.cuda.device(dev):
+            st = fn(*args, p, n, stream)
+    if st:
+        raise DllmError(st, where)
 
 
 def dllm_rope_table(table, theta: float, stream=None):
     """table [N, head_dim/2, 2] float32 <- cos, sin of the rotation angles."""
-    import torch
-    _want("table", table, torch.float32, table.device, (None, None, 2))
-    with _on(table.device):
+    dev = table.get_device()
+    if (table.dtype is not _F32 or dev < 0 or table.dim() != 3 or table.shape[2] != 2
+            or not table.is_contiguous()):
+        _bad([("table", table, (_F32,), (None, None, 2))], dev)
+    with torch.cuda.device(dev):
         st = _rope_table(ptr(table), table.shape[0], 2 * table.shape[1], float(theta),
                          _stream(stream))
     _check(st, "dllm_rope_table")
@@ -456,97 +508,100 @@ def dllm_qk_norm_rope(q, k, q_gain, k_gain, rope, q_out, k_out, idx, count, eps:
     [B, N, n_kv_heads, head_dim] cache whose rows at the positions are meant; rope: a
     dllm_rope_table or None; idx [B, k_cap] and count [B] as for dllm_partial_layer.  The
     number of positions N comes from a cache or the table."""
-    import torch
-    dev, dt = q.device, q.dtype
-    hd = q_gain.shape[0]
-    code = _dtype_code(q)
+    code, dt, dev, hd = _dtype_code(q), q.dtype, q.get_device(), q_gain.shape[0]
     if idx is None and count is None:
         raise ValueError("idx or count: the number of sequences is theirs")
     B = (idx if idx is not None else count).shape[0]
-    caches = [t.shape[1] for t in (k, k_out) if t.dim() == 4]
+    k_in, k_to = k.dim() == 4, k_out.dim() == 4
     if N is None:
-        N = caches[0] if caches else rope.shape[0]
+        N = k.shape[1] if k_in else k_out.shape[1] if k_to else rope.shape[0]
     wq = q.shape[1]
-    wk = k.shape[2] * hd if k.dim() == 4 else k.shape[1]
-    for name, t, w in (("q", q, wq), ("q_out", q_out, wq), ("k", k, wk), ("k_out", k_out, wk)):
-        if t.dim() == 4:
-            _want(name, t, dt, dev, (B, N, wk // hd, hd))
-        else:
-            _want(name, t, dt, dev, rows_of=w)
-    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
-        _want(name, t, dt, dev, (hd,))
-    if rope is not None:
-        _want("rope", rope, torch.float32, dev, (None, hd // 2, 2))
-        if rope.shape[0] < N:
+    wk = k.shape[2] * hd if k_in else k.shape[1]
+    rows = min(q.shape[0], q_out.shape[0], q.shape[0] if k_in else k.shape[0],
+               q.shape[0] if k_to else k_out.shape[0])
+    ldq, ldqo = _rows_fit(q, dt, wq, dev), _rows_fit(q_out, dt, wq, dev)
+    cache = (B, N, wk // hd, hd)
+
+    def kept(t, is_cache):
+        if not is_cache:
+            return _rows_fit(t, dt, wk, dev)
+        return int(t.shape == cache and t.dtype is dt and t.is_contiguous() and t.get_device() == dev)
+
+    ldk, ldko = kept(k, k_in), kept(k_out, k_to)
+    k_cap = _lists_fit(idx, count, B, rows, dev)
+    if not (ldq and ldqo and ldk and ldko and k_cap and dev >= 0 and wq % hd == 0 and wk % hd == 0
+            and q_gain.dtype is dt and k_gain.dtype is dt and k_gain.shape == (hd,)
+            and q_gain.dim() == 1 and q_gain.get_device() == dev and k_gain.get_device() == dev
+            and q_gain.is_contiguous() and k_gain.is_contiguous()
+            and (rope is None or (rope.dtype is _F32 and rope.get_device() == dev
+                                  and rope.is_contiguous() and rope.shape[1:] == (hd // 2, 2)
+                                  and rope.shape[0] >= N))):
+        if wq % hd or wk % hd:
+            raise ValueError(f"rows of {wq} and {wk} elements for heads of {hd}")
+        if rope is not None and rope.dim() == 3 and rope.shape[0] < N:
             raise ValueError(f"rope: {rope.shape[0]} positions, wanted {N}")
-    if wq % hd or wk % hd:
-        raise ValueError(f"rows of {wq} and {wk} elements for heads of {hd}")
-    k_cap = _row_lists(idx, count, dev, B, min(t.shape[0] for t in (q, q_out, k, k_out)
-                                               if t.dim() == 2))
-    with _on(dev):
-        st = _qk_norm(ptr(q), _ld(q), ptr(k), 0 if k.dim() == 4 else _ld(k), int(k.dim() == 4),
-                      ptr(q_gain), ptr(k_gain), ptr(rope), ptr(q_out), _ld(q_out), ptr(k_out),
-                      0 if k_out.dim() == 4 else _ld(k_out), int(k_out.dim() == 4), ptr(idx),
-                      ptr(count), k_cap, B, N, wq // hd, wk // hd, hd, float(eps), code,
-                      ws.ptr if ws else None, ws.nbytes if ws else 0, _stream(stream))
-    _check(st, "dllm_qk_norm_rope")
+        _bad([("q", q, (dt,), ("rows", wq)), ("q_out", q_out, (dt,), ("rows", wq)),
+              ("k", k, (dt,), cache if k_in else ("rows", wk)),
+              ("k_out", k_out, (dt,), cache if k_to else ("rows", wk)),
+              ("q_gain", q_gain, (dt,), (hd,)), ("k_gain", k_gain, (dt,), (hd,)),
+              ("rope", rope, (_F32,), (None, hd // 2, 2))]
+             + _list_checks(idx, count, B), dev)
+    _launch(dev, _qk_norm, (q.data_ptr(), ldq, k.data_ptr(), ldk, k_in, q_gain.data_ptr(),
+                            k_gain.data_ptr(), ptr(rope), q_out.data_ptr(), ldqo,
+                            k_out.data_ptr(), ldko, k_to, ptr(idx), ptr(count), k_cap, B, N,
+                            wq // hd, wk // hd, hd, eps, code), ws, stream, "dllm_qk_norm_rope")
 
 
 def dllm_kv8_scale_count(B: int, N: int, n_kv_heads: int, block: int) -> int:
     return int(_kv8_scales(B, N, n_kv_heads, block))
 
 
-def _kv8_cache(k8, k_scale, v8, v_scale, block: int):
-    import torch
-    B, N, H, hd = k8.shape
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    nblk = -(-N // block) if block > 0 else 0
-    for name, t in (("k8", k8), ("v8", v8)):
-        _want(name, t, codes, k8.device, (B, N, H, hd))
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _want(name, t, torch.float32, k8.device, (B, H, nblk))
-    return B, N, H, hd
-
-
 def kv8_cache(B: int, N: int, n_kv_heads: int, head_dim: int, block: int, device="cuda"):
     """An empty 8-bit cache: codes [B, N, n_kv_heads, head_dim] (float8_e4m3fn) and scales
     [B, n_kv_heads, ceil(N/block)] of zeros, as (k8, k_scale, v8, v_scale)."""
-    import torch
-    code = lambda: torch.zeros(B, N, n_kv_heads, head_dim, dtype=torch.uint8,
-                               device=device).view(torch.float8_e4m3fn)
-    scale = lambda: torch.zeros(B, n_kv_heads, -(-N // block), device=device)
+
+    def code():
+        return torch.zeros(B, N, n_kv_heads, head_dim, dtype=torch.uint8,
+                           device=device).view(torch.float8_e4m3fn)
+
+    def scale():
+        return torch.zeros(B, n_kv_heads, -(-N // block), device=device)
     return code(), scale(), code(), scale()
+
+
+def _kv8_rows_call(fn, where, k, v, idx, count, k8, k_scale, v8, v_scale, block, ws, stream, reads):
+    shape = k8.shape
+    B, N, H, hd = shape
+    nblk, dev, w = -(-N // max(block, 1)), k8.get_device(), H * hd
+    ldk, ldv = _rows_fit(k, _BF16, w, dev), _rows_fit(v, _BF16, w, dev)
+    rows = min(k.shape[0], v.shape[0])
+    k_cap = _lists_fit(idx, count, B, rows, dev)
+    if not (ldk and ldv and k_cap and _cache_fits(k8, k_scale, v8, v_scale, shape, (B, H, nblk), dev)):
+        if B and rows < B * (idx.shape[1] if idx is not None else 1):
+            raise ValueError(f"compact tensors of {rows} rows for {B} sequences")
+        bf = (_BF16,)
+        _bad([("k", k, bf, ("rows", w)), ("v", v, bf, ("rows", w))]
+             + _kv8_checks(k8, k_scale, v8, v_scale, B, N, H, hd, nblk)
+             + _list_checks(idx, count, B), dev)
+    lists = (ptr(idx), ptr(count), k_cap, B, N, H, hd, block)
+    cache = (k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(), v_scale.data_ptr())
+    kv = (k.data_ptr(), ldk, v.data_ptr(), ldv)
+    _launch(dev, fn, cache + lists + kv if reads else kv + lists + cache, ws, stream, where)
 
 
 def dllm_kv8_write(k, v, idx, count, k8, k_scale, v8, v_scale, block: int, ws: Workspace = None,
                    stream=None):
     """K/V rows [rows, n_kv_heads*head_dim] bf16 into the 8-bit cache at the positions idx
     [B, k_cap] (None: row j at position j), count [B] of them (None: all)."""
-    import torch
-    B, N, H, hd = _kv8_cache(k8, k_scale, v8, v_scale, block)
-    for name, t in (("k", k), ("v", v)):
-        _want(name, t, torch.bfloat16, k8.device, rows_of=H * hd)
-    k_cap = _row_lists(idx, count, k8.device, B, min(k.shape[0], v.shape[0]))
-    with _on(k8.device):
-        st = _kv8_write(ptr(k), _ld(k), ptr(v), _ld(v), ptr(idx), ptr(count), k_cap, B, N, H, hd,
-                        int(block), ptr(k8), ptr(k_scale), ptr(v8), ptr(v_scale),
-                        ws.ptr if ws else None, ws.nbytes if ws else 0, _stream(stream))
-    _check(st, "dllm_kv8_write")
+    _kv8_rows_call(_kv8_write, "dllm_kv8_write", k, v, idx, count, k8, k_scale, v8, v_scale, block,
+                   ws, stream, False)
 
 
 def dllm_kv8_read(k8, k_scale, v8, v_scale, idx, count, k_out, v_out, block: int,
                   ws: Workspace = None, stream=None):
     """Rows of the 8-bit cache as bf16 compact rows [rows, n_kv_heads*head_dim]."""
-    import torch
-    B, N, H, hd = _kv8_cache(k8, k_scale, v8, v_scale, block)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _want(name, t, torch.bfloat16, k8.device, rows_of=H * hd)
-    k_cap = _row_lists(idx, count, k8.device, B, min(k_out.shape[0], v_out.shape[0]))
-    with _on(k8.device):
-        st = _kv8_read(ptr(k8), ptr(k_scale), ptr(v8), ptr(v_scale), ptr(idx), ptr(count), k_cap,
-                       B, N, H, hd, int(block), ptr(k_out), _ld(k_out), ptr(v_out), _ld(v_out),
-                       ws.ptr if ws else None, ws.nbytes if ws else 0, _stream(stream))
-    _check(st, "dllm_kv8_read")
+    _kv8_rows_call(_kv8_read, "dllm_kv8_read", k_out, v_out, idx, count, k8, k_scale, v8, v_scale,
+                   block, ws, stream, True)
 
 
 def dllm_attention_kv8_workspace_size(B, k_cap, N, n_heads, n_kv_heads, head_dim) -> int:
@@ -558,31 +613,34 @@ def dllm_attention_kv8(q, k8, k_scale, v8, v_scale, o, count, k_cap: int, block:
     """Attention of compact query rows [B*k_cap, n_heads*head_dim] over the 8-bit cache (the
     first kv_len[b] positions of each sequence); returns the workspace, to be kept for the
     next call of these sizes."""
-    import torch
-    B, N, H, hd = _kv8_cache(k8, k_scale, v8, v_scale, block)
-    dev = k8.device
-    wq = q.shape[1]
-    for name, t in (("q", q), ("o", o)):
-        _want(name, t, torch.bfloat16, dev, (None, wq))
-        if t.shape[0] < B * k_cap:
-            raise ValueError(f"{name}: {t.shape[0]} rows for {B} sequences of {k_cap}")
-    if wq % hd:
-        raise ValueError(f"rows of {wq} elements for heads of {hd}")
-    for name, t in (("count", count), ("kv_len", kv_len)):
-        if t is not None:
-            _want(name, t, torch.int32, dev, (B,))
-    for name, t in (("m", m), ("l", l)):
-        if t is not None:
-            _want(name, t, torch.float32, dev, (None, wq // hd))
-            if t.shape[0] < B * k_cap:
+    bf16, shape, dev = _BF16, k8.shape, k8.get_device()
+    B, N, H, hd = shape
+    R, wq = q.shape
+    nblk, Hq = -(-N // max(block, 1)), wq // hd
+    if not (q.dtype is bf16 and o.dtype is bf16 and o.shape[1:] == (wq,) and R >= B * k_cap
+            and o.shape[0] >= B * k_cap and q.is_contiguous() and o.is_contiguous()
+            and q.get_device() == dev and o.get_device() == dev and wq % hd == 0
+            and _lists_fit(None, count, B, R, dev) and (kv_len is None or _lists_fit(None, kv_len, B, R, dev))
+            and (m is None or (m.dtype is _F32 and m.shape[1:] == (Hq,) and m.is_contiguous()
+                               and m.shape[0] >= B * k_cap and m.get_device() == dev))
+            and (l is None or (l.dtype is _F32 and l.shape[1:] == (Hq,) and l.is_contiguous()
+                               and l.shape[0] >= B * k_cap and l.get_device() == dev))
+            and _cache_fits(k8, k_scale, v8, v_scale, shape, (B, H, nblk), dev)):
+        if wq % hd:
+            raise ValueError(f"rows of {wq} elements for heads of {hd}")
+        for name, t in (("q", q), ("o", o), ("m", m), ("l", l)):
+            if t is not None and t.shape[0] < B * k_cap:
                 raise ValueError(f"{name}: {t.shape[0]} rows for {B} sequences of {k_cap}")
+        bf, f32 = (bf16,), (_F32,)
+        _bad([("q", q, bf, (None, wq)), ("o", o, bf, (None, wq)), ("m", m, f32, (None, Hq)),
+              ("l", l, f32, (None, Hq))] + _kv8_checks(k8, k_scale, v8, v_scale, B, N, H, hd, nblk)
+             + _list_checks(None, count, B) + _list_checks(None, kv_len, B), dev)
     if ws is None:
-        ws = Workspace(dllm_attention_kv8_workspace_size(B, k_cap, N, wq // hd, H, hd), dev)
-    with _on(dev):
-        st = _attn_kv8(ptr(q), ptr(k8), ptr(k_scale), ptr(v8), ptr(v_scale), ptr(o), ptr(m),
-                       ptr(l), ptr(count), ptr(kv_len), B, int(k_cap), N, wq // hd, H, hd,
-                       int(block), ws.ptr, ws.nbytes, _stream(stream))
-    _check(st, "dllm_attention_kv8")
+        ws = Workspace(dllm_attention_kv8_workspace_size(B, k_cap, N, Hq, H, hd), k8.device)
+    _launch(dev, _attn_kv8, (q.data_ptr(), k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(),
+                             v_scale.data_ptr(), o.data_ptr(), ptr(m), ptr(l), ptr(count),
+                             ptr(kv_len), B, k_cap, N, Hq, H, hd, block), ws, stream,
+            "dllm_attention_kv8")
     return ws
 
 
