@@ -43,38 +43,40 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 constexpr int kKv8TcRows = 16;
 constexpr int RW = 4;        // warps per CTA
 constexpr int RM = 16;       // packed query rows per CTA
-constexpr int RK = 16;       // keys per warp and turn
+constexpr int RK = 16;       // keys per warp and tile
 
 template <int HD>
 struct RowsSmem {
   static constexpr int VB = HD / 8;                     // V bytes per lane and key
-  static constexpr int V_OFF = 32 * (HD / 2);           // K codes of 16 keys, then V's,
-  static constexpr int SC_OFF = V_OFF + 32 * 4 * VB;    // then the two scales
-  static constexpr int STAGE = SC_OFF + 16;
-  static constexpr int STAGES = HD == 128 ? 5 : 8;
-  static constexpr int WARP = STAGE * STAGES;
-  static constexpr int RED = RW * RM * HD * 4;          // outputs of the warps
-  static constexpr int ML_OFF = RW * WARP > RED ? RW * WARP : RED;
-  static constexpr int TOTAL = ML_OFF + RW * RM * 2 * 4;
+  static constexpr int TILE = RW * RK * HD;             // codes of 64 keys
+  static constexpr int STAGES = HD == 128 ? 4 : 6;      // of a K and a V tile each
+  static constexpr int RED = RW * RM * HD * 4;          // outputs of the warps, over the ring
+  static constexpr int RING = STAGES * 2 * TILE > RED ? STAGES * 2 * TILE : RED;
+  static constexpr int ML_OFF = RING;
+  static constexpr int BAR_OFF = ML_OFF + RW * RM * 2 * 4;
+  static constexpr int TOTAL = BAR_OFF + (2 * STAGES + 1) * 8;
+  static_assert(3 * (TOTAL + 1024) <= 228 * 1024, "three CTAs per SM");
 };
 
 // One CTA = up to 16 packed query rows of one (sequence, kv head) and one share of
-// the keys; its warps take 16 keys each in turn.  A warp's codes go through a ring
-// of cp.async copies in shared memory in which every lane reads back what it
-// copied itself, laid out so that a lane's 16 bytes are its mma fragments: K along
-// the head (any order of the inner index serves a product as long as Q has the
-// same), V by gathering one byte of two neighbouring keys.  The codes are thus
-// read once, converted in registers (one cvt per two codes), and never written
-// back.
+// the keys.  Tiles of 64 keys of K and V come by TMA (swizzled, so that the reads
+// below are free of bank conflicts at head_dim 128); each warp takes 16 keys of
+// every tile.  The codes are read straight into mma.sync fragments and converted in
+// registers (one cvt per two codes): K along the head, 16 codes of a lane in an
+// order of the inner index that Q's fragments share; V by gathering one byte of two
+// keys.  With so few rows the tensor cores' rate does not matter and the kernel is
+// bound by the codes' way: 2 bytes per key and head_dim element.
 template <int HD>
-__global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A) {
+__global__ void __launch_bounds__(RW * 32, 3)
+    attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const Kv8Args A) {
   griddep_launch_dependents();
   griddep_wait();
   using L = RowsSmem<HD>;
   constexpr int KS = HD / 16;    // k-steps of Q K^T
   constexpr int NT = HD / 8;     // n-tiles of P V
   constexpr int KV16 = HD / 64;  // 16-byte pieces of a key row per lane
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   int u = blockIdx.x;
@@ -94,45 +96,61 @@ __global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A)
     len = min(max(want, 0), N);
     if (len != want && threadIdx.x == 0) raise_status(A.rows.status, DEV_BAD_SHAPE);
   }
-  const int chunks = (len + RK - 1) / RK;
-  const int per = (chunks + A.S - 1) / A.S;
-  const int c_lo = min(chunks, share * per), c_hi = min(chunks, c_lo + per);
+  const int all = (len + RW * RK - 1) / (RW * RK);
+  const int per = (all + A.S - 1) / A.S;
+  const int t_lo = min(all, share * per);
+  const int T = min(all, t_lo + per) - t_lo;  // this CTA's tiles
 
-  const uint32_t ring = smem_u32(smem) + warp * L::WARP;
-  const uint8_t* kbase = A.k8 + ((size_t)b * N * A.Hkv + kvh) * HD;
-  const uint8_t* vbase = A.v8 + ((size_t)b * N * A.Hkv + kvh) * HD;
-  const size_t row_bytes = (size_t)A.Hkv * HD;
-  const size_t sc0 = ((size_t)b * A.Hkv + kvh) * A.nblk;
-  // keys past the last one arrive as zeros (copies of 0 bytes from a valid row)
-  auto issue = [&](int c, int slot) {
-    if (c < c_hi) {
-      const uint32_t st = ring + slot * L::STAGE;
-      const int k0 = c * RK;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int key = k0 + n * 8 + g;
-        const uint8_t* src = kbase + (size_t)min(key, len - 1) * row_bytes + t * 16;
-#pragma unroll
-        for (int i = 0; i < KV16; ++i)
-          cp_async16(st + ((n * KV16 + i) * 32 + lane) * 16, src + i * 64, key < len);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = k0 + 2 * t + (i & 1) + (i >> 1) * 8;
-        const uint8_t* src = vbase + (size_t)min(key, len - 1) * row_bytes + g * L::VB;
-        if constexpr (HD == 128)
-          cp_async16(st + L::V_OFF + (i * 32 + lane) * 16, src, key < len);
-        else
-          cp_async8(st + L::V_OFF + (i * 32 + lane) * 8, src, key < len);
-      }
-      if (lane < 2)
-        cp_async4(st + L::SC_OFF + lane * 4, (lane == 0 ? A.ks : A.vs) + sc0 + (k0 >> A.blk_log2));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&bars[2 * L::STAGES]);
+  auto full = [&](int st) { return smem_u32(&bars[st]); };
+  auto empty = [&](int st) { return smem_u32(&bars[L::STAGES + st]); };
+  const uint32_t ring = smem_u32(smem);
+  int* const status = A.rows.status;
+  if (ring & 1023u) {  // the swizzle counts from multiples of 1024
+    if (threadIdx.x == 0) raise_status(status, DEV_BAD_SHAPE);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    if (T > 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
     }
-    cp_commit();
+    for (int i = 0; i < L::STAGES; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), RW);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  // tile i (from one thread): K, then V, into stage i % STAGES
+  int issued = 0;
+  auto issue = [&](int i) {
+    const int st = i % L::STAGES;
+    if (i >= L::STAGES && !mbar_wait(empty(st), (i / L::STAGES - 1) & 1, abort_flag, status)) return;
+    mbar_arrive_expect_tx(full(st), 2 * L::TILE);
+    const uint32_t dst = ring + st * 2 * L::TILE;
+    const int key = (t_lo + i) * RW * RK;
+    tma_load_3d(dst, &tmK, full(st), kvh * HD, key, b);
+    tma_load_3d(dst + L::TILE, &tmV, full(st), kvh * HD, key, b);
+    issued = i + 1;
   };
-  // the ring's first copies are on their way before the queries are read
-#pragma unroll
-  for (int i = 0; i < L::STAGES - 1; ++i) issue(c_lo + warp + i * RW, i);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < min(T, L::STAGES); ++i) issue(i);
+
+  // the scales of this warp's keys, read a tile ahead
+  const size_t sc0 = ((size_t)b * A.Hkv + kvh) * A.nblk;
+  auto scales_of = [&](int i) {
+    const int key = ((t_lo + i) * RW + warp) * RK;
+    float2 f = make_float2(0.f, 0.f);
+    if (i < T && key < len) {
+      f.x = __ldg(A.ks + sc0 + (key >> A.blk_log2));
+      f.y = __ldg(A.vs + sc0 + (key >> A.blk_log2));
+    }
+    return f;
+  };
+  float2 next = scales_of(0);
 
   // Q fragments of packed rows g and g + 8: in k-step i of a half of 64 elements, lane
   // t holds elements 16 t + 4 i .. + 3
@@ -182,97 +200,136 @@ __global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A)
   for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  int slot = 0;
-  for (int c = c_lo + warp; c < c_hi; c += RW) {
-    cp_wait<L::STAGES - 2>();
-    __syncwarp();
-    issue(c + (L::STAGES - 1) * RW, slot == 0 ? L::STAGES - 1 : slot - 1);
-    const uint8_t* st = smem + warp * L::WARP + slot * L::STAGE;
-    if (++slot == L::STAGES) slot = 0;
-    const float2 sc = *reinterpret_cast<const float2*>(st + L::SC_OFF);
-    float s[2][4];
+  // Column n of an 8-key score tile is key key8(n): at head_dim 128 rows 4 apart in
+  // neighbouring lanes, whose swizzled 16-byte pieces lie on different banks; V's 16-byte
+  // pieces are dealt out the same way.  (At head_dim 64 a row is half a line: in order.)
+  auto key8 = [](int n) { return HD == 128 ? (n & 1) * 4 + (n >> 1) : n; };
+  auto piece8 = [](int n) { return HD == 128 ? (n & 1) * 4 + (n >> 1) : n; };
+  // address of piece p (16 bytes) of key row r of a tile, as TMA's swizzle leaves it
+  auto at = [](int r, int p) {
+    return HD == 128 ? r * 128 + ((p ^ (r & 7)) << 4) : r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
+  };
+  uint32_t k_at[2][KV16], v_at[4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int p = 0; p < KV16; ++p) k_at[n][p] = at(warp * RK + 8 * n + key8(g), 4 * p + t);
+  int v_key[4];  // of this lane's V fragments, within the warp's 16
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v_key[i] = 8 * (i >> 1) + key8(2 * t + (i & 1));
+    const int r = warp * RK + v_key[i];
+    v_at[i] = L::TILE + (HD == 128 ? at(r, piece8(g)) : at(r, g >> 1) + (g & 1) * 8);
+  }
+
+  bool ok = true;
+  for (int i = 0; i < T; ++i) {
+    const int st = i % L::STAGES;
+    const float2 sc = next;
+    next = scales_of(i + 1);
+    // the stage that the tile before last freed
+    if (threadIdx.x == 0 && i >= 2 && i + L::STAGES - 2 < T) issue(i + L::STAGES - 2);
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, mbar_wait(full(st), (i / L::STAGES) & 1, abort_flag, status));
+    if (!ok) break;
+    const uint32_t base = ring + st * 2 * L::TILE;
+    const int left = len - ((t_lo + i) * RW + warp) * RK;  // of this warp's keys that exist
+    if (left > 0) {
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
       for (int p = 0; p < KV16; ++p) {
-        const uint4 w = *reinterpret_cast<const uint4*>(st + ((n * KV16 + p) * 32 + lane) * 16);
-        const uint32_t q4[4] = {w.x, w.y, w.z, w.w};
+        uint32_t q4[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) lds128(q4[n], base + k_at[n][p]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          mma_f16(s[n], qf[p * 4 + e], e4m3x2_to_f16x2(q4[e] & 0xffffu), e4m3x2_to_f16x2(q4[e] >> 16));
-      }
-    }
-    float ev, inv_v;
-    v_scale_parts(sc.y, ev, inv_v);
-    const float k0 = rs[0] * sc.x, k1 = rs[1] * sc.x;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      s[n][0] = fmaf(s[n][0], k0, ev), s[n][1] = fmaf(s[n][1], k0, ev);
-      s[n][2] = fmaf(s[n][2], k1, ev), s[n][3] = fmaf(s[n][3], k1, ev);
-    }
-    if ((c + 1) * RK > len) {
+          for (int n = 0; n < 2; ++n) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16x4(q4[n][e], lo, hi);
+            mma_f16(s[n], qf[p * 4 + e], lo, hi);
+          }
+      }
+      uint32_t w[4][L::VB / 4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if constexpr (HD == 128)
+          lds128(w[x], base + v_at[x]);
+        else
+          lds64(w[x], base + v_at[x]);
+      }
+      float ev, inv_v;
+      v_scale_parts(sc.y, ev, inv_v);
+      const float k0 = rs[0] * sc.x, k1 = rs[1] * sc.x;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = fmaf(s[n][0], k0, ev), s[n][1] = fmaf(s[n][1], k0, ev);
+        s[n][2] = fmaf(s[n][2], k1, ev), s[n][3] = fmaf(s[n][3], k1, ev);
+      }
+      if (left < RK) {  // what lies past the last key plays no part, whatever it holds
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (8 * n + key8(2 * t + (x & 1)) >= left) s[n][x] = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y < L::VB / 4; ++y)
+            if (v_key[x] >= left) w[x][y] = 0;
+      }
+      float alpha[2] = {1.f, 1.f};
+      bool grew = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (mx > m[x] + kKv8Lazy) {
+          alpha[x] = exp2_approx(m[x] - mx);
+          m[x] = mx;
+          grew = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+        l[0] *= alpha[0], l[1] *= alpha[1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          o[n][0] *= alpha[0], o[n][1] *= alpha[0], o[n][2] *= alpha[1], o[n][3] *= alpha[1];
+      }
+      float p[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c * RK + n * 8 + 2 * t + (i & 1) >= len) s[n][i] = -INFINITY;
-    }
-    float alpha[2] = {1.f, 1.f};
-    bool grew = false;
+        for (int x = 0; x < 4; ++x) p[n][x] = exp2_approx(s[n][x] - m[x >> 1]);
+      l[0] = fmaf((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]), inv_v, l[0]);
+      l[1] = fmaf((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]), inv_v, l[1]);
+      const uint32_t pa[4] = {pack_h2(p[0][0], p[0][1]), pack_h2(p[0][2], p[0][3]),
+                              pack_h2(p[1][0], p[1][1]), pack_h2(p[1][2], p[1][3])};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (mx > m[i] + kKv8Lazy) {
-        alpha[i] = exp2_approx(m[i] - mx);
-        m[i] = mx;
-        grew = true;
+      for (int q = 0; q < L::VB / 4; ++q) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // bytes 4 q + 2 j, + 1 of the pieces: (key, key) pairs
+          const uint32_t a = __byte_perm(w[0][q], w[1][q], j ? 0x7362 : 0x5140);
+          const uint32_t d = __byte_perm(w[2][q], w[3][q], j ? 0x7362 : 0x5140);
+          uint32_t v[4];
+          e4m3x4_to_f16x4(a, v[0], v[2]);
+          e4m3x4_to_f16x4(d, v[1], v[3]);
+          mma_f16(o[q * 4 + 2 * j], pa, v[0], v[1]);
+          mma_f16(o[q * 4 + 2 * j + 1], pa, v[2], v[3]);
+        }
       }
     }
-    if (__any_sync(0xffffffffu, grew)) {
-      l[0] *= alpha[0], l[1] *= alpha[1];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        o[n][0] *= alpha[0], o[n][1] *= alpha[0], o[n][2] *= alpha[1], o[n][3] *= alpha[1];
-    }
-    float p[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[n][i] = exp2_approx(s[n][i] - m[i >> 1]);
-    l[0] = fmaf((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]), inv_v, l[0]);
-    l[1] = fmaf((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]), inv_v, l[1]);
-    const uint32_t pa[4] = {pack_h2(p[0][0], p[0][1]), pack_h2(p[0][2], p[0][3]),
-                            pack_h2(p[1][0], p[1][1]), pack_h2(p[1][2], p[1][3])};
-    uint32_t w[4][L::VB / 4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t* src = st + L::V_OFF + (i * 32 + lane) * L::VB;
-      if constexpr (HD == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(src);
-        w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(src);
-        w[i][0] = x.x, w[i][1] = x.y;
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < L::VB / 4; ++q) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {  // columns 4 q + 2 j, + 1: (key, next key) byte pairs
-        const uint32_t a = __byte_perm(w[0][q], w[1][q], j ? 0x7362 : 0x5140);
-        const uint32_t d = __byte_perm(w[2][q], w[3][q], j ? 0x7362 : 0x5140);
-        const uint32_t v[4] = {e4m3x2_to_f16x2(a & 0xffffu), e4m3x2_to_f16x2(d & 0xffffu),
-                         e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(d >> 16)};
-        mma_f16(o[q * 4 + 2 * j], pa, v[0], v[1]);
-        mma_f16(o[q * 4 + 2 * j + 1], pa, v[2], v[3]);
-      }
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty(st));
   }
-  cp_wait<0>();
-  __syncthreads();  // every ring is done with: the warps' outputs take its place
+  if (!ok && threadIdx.x == 0)  // a wait ran out: the copies on their way land before the exit
+    for (int i = max(0, issued - L::STAGES); i < issued; ++i)
+      mbar_wait_drain(full(i % L::STAGES), (i / L::STAGES) & 1, status);
+  __syncthreads();  // every tile has been read: the warps' outputs take the ring's place
+  if (*abort_flag) return;
 
   float* red = reinterpret_cast<float*>(smem);
   float* ml = reinterpret_cast<float*>(smem + L::ML_OFF);
@@ -285,13 +342,13 @@ __global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A)
       float* x = ml + (warp * RM + g + 8 * i) * 2;
       x[0] = m[i], x[1] = sum;
     }
-    // n-tile j of lane t: columns 2t * VB + j and (2t + 1) * VB + j
-    float* dst = red + (warp * RM + g + 8 * i) * HD + 2 * t * L::VB;
+    // n-tile j of lane t: byte j of V's pieces piece8(2t) and piece8(2t + 1)
+    float* dst = red + (warp * RM + g + 8 * i) * HD;
 #pragma unroll
     for (int j = 0; j < NT; j += 4) {
-      *reinterpret_cast<float4*>(dst + j) =
+      *reinterpret_cast<float4*>(dst + piece8(2 * t) * L::VB + j) =
           make_float4(o[j][2 * i], o[j + 1][2 * i], o[j + 2][2 * i], o[j + 3][2 * i]);
-      *reinterpret_cast<float4*>(dst + L::VB + j) = make_float4(
+      *reinterpret_cast<float4*>(dst + piece8(2 * t + 1) * L::VB + j) = make_float4(
           o[j][2 * i + 1], o[j + 1][2 * i + 1], o[j + 2][2 * i + 1], o[j + 3][2 * i + 1]);
     }
   }
@@ -343,7 +400,9 @@ __global__ void __launch_bounds__(RW * 32) attn_kv8_rows_kernel(const Kv8Args A)
 }
 
 // The shares of one output row, in share order: M = max m_s, w_s = l_s 2^(m_s - M),
-// O = sum w_s o_s / sum w_s.  One warp per (row, head); an empty share has l = 0.
+// O = sum w_s o_s / sum w_s.  One warp per (row, head); lanes hold the weights of 32
+// shares at a time, and 8 shares' slices are on their way at once (one after the
+// other, 64 shares took 20 us).  An empty share has l = 0 and no slice.
 template <int HD>
 __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   constexpr int PER = HD / 32;
@@ -355,23 +414,47 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   kv8_seq_rows(A.rows, A.rows.B - 1, off, cnt);
   if (u >= (size_t)(off + cnt) * A.Hq) return;
   const size_t stride = (size_t)A.part_rows * A.Hq;
+  float2 ml[kKv8MaxShares / 32];
   float mx = -INFINITY;
-  for (int s = lane; s < A.S; s += 32) {
-    const float2 x = *reinterpret_cast<const float2*>(A.part_ml + (s * stride + u) * 2);
-    if (x.y != 0.f) mx = fmaxf(mx, x.x);
+#pragma unroll
+  for (int i = 0; i < kKv8MaxShares / 32; ++i) {
+    ml[i] = make_float2(-INFINITY, 0.f);
+    if (lane + 32 * i < A.S)
+      ml[i] = *reinterpret_cast<const float2*>(A.part_ml + ((lane + 32 * i) * stride + u) * 2);
+    if (ml[i].y != 0.f) mx = fmaxf(mx, ml[i].x);
   }
   mx = warp_max(mx);
   float acc[PER], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  for (int s = 0; s < A.S; ++s) {
-    const float2 x = *reinterpret_cast<const float2*>(A.part_ml + (s * stride + u) * 2);
-    if (x.y == 0.f) continue;
-    const float w = x.y * exp2_approx(x.x - mx);
-    sum += w;
-    const float* src = A.part_o + (s * stride + u) * HD + lane * PER;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, src[i], acc[i]);
+  for (int i = 0; i < kKv8MaxShares / 32; ++i) {
+    if (32 * i >= A.S) break;
+    const float mine = ml[i].y == 0.f ? 0.f : ml[i].y * exp2_approx(ml[i].x - mx);
+    for (int s0 = 32 * i; s0 < min(A.S, 32 * i + 32); s0 += 8) {
+      float w[8], o[8][PER];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = __shfl_sync(0xffffffffu, mine, (s0 + k) & 31);
+      // every load is issued (from some share's slice) and what an empty share holds dropped
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float* src = A.part_o + (min(s0 + k, A.S - 1) * stride + u) * HD + lane * PER;
+        if constexpr (PER == 4)
+          *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(src);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int x = 0; x < PER; ++x) o[k][x] = w[k] != 0.f ? o[k][x] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += w[k];
+#pragma unroll
+        for (int x = 0; x < PER; ++x) acc[x] = fmaf(w[k], o[k][x], acc[x]);
+      }
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   __nv_bfloat16* dst = A.o + u * HD + lane * PER;
@@ -401,8 +484,8 @@ Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd,
   const int least = pl.tc ? 128 : 256;  // keys that a share holds at least
   pl.tiles = (int)((packed + rows - 1) / rows);
   const long long units = (long long)B * Hkv * pl.tiles;
-  const long long want = std::max(1LL, 2LL * num_sms() / std::max(1LL, units));  // two CTAs per SM
-  pl.shares = (int)std::max(1LL, std::min({want, (long long)(keys + least - 1) / least, 64LL}));
+  const long long want = std::max(1LL, (pl.tc ? 2LL : 3LL) * num_sms() / std::max(1LL, units));  // CTAs that share an SM
+  pl.shares = (int)std::max(1LL, std::min({want, (long long)(keys + least - 1) / least, (long long)kKv8MaxShares}));
   while (pl.shares > 1 && part_floats(pl.shares, M_cap, Hq, hd) * sizeof(float) > part_bytes) --pl.shares;
   pl.ctas = units * pl.shares;
   return pl;
@@ -435,14 +518,18 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   A.part_o = part;
   A.part_ml = pl.shares > 1 ? part + (size_t)pl.shares * m.M_cap * Hq * hd : nullptr;
   A.st_m = st_m, A.st_l = st_l;
+  // (no position cached: nothing is copied, and the maps point nowhere)
+  CUtensorMap tk{}, tv{};
+  if (m.N > 0 && (!tmap_codes(&tk, k8, m.B, m.N, Hkv * hd, hd, 64) || !tmap_codes(&tv, v8, m.B, m.N, Hkv * hd, hd, 64)))
+    return cudaErrorInvalidValue;
   cudaError_t e;
   {
     ProfScope prof("attention_kv8", s);
     if (pl.tc)
       e = launch_attention_kv8_tc(A, pl.ctas, hd, s);
     else
-      e = hd == 128 ? launch_kv8<attn_kv8_rows_kernel<128>>((unsigned)pl.ctas, RW * 32, RowsSmem<128>::TOTAL, s, A)
-                  : launch_kv8<attn_kv8_rows_kernel<64>>((unsigned)pl.ctas, RW * 32, RowsSmem<64>::TOTAL, s, A);
+      e = hd == 128 ? launch_kv8<attn_kv8_rows_kernel<128>>((unsigned)pl.ctas, RW * 32, RowsSmem<128>::TOTAL, s, tk, tv, A)
+                  : launch_kv8<attn_kv8_rows_kernel<64>>((unsigned)pl.ctas, RW * 32, RowsSmem<64>::TOTAL, s, tk, tv, A);
   }
   if (e != cudaSuccess || pl.shares == 1) return e;
   ProfScope prof("attention_kv8_merge", s);

@@ -10,6 +10,8 @@ namespace dllm {
 constexpr float kKv8Log2e = 1.4426950408889634f;
 constexpr float kKv8Lazy = 8.0f;  // how far below the largest x_j the reference may stay
 
+constexpr int kKv8MaxShares = 64;
+
 struct Kv8Args {
   const __nv_bfloat16* q;
   const uint8_t* k8;
@@ -86,11 +88,21 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void lds128(uint32_t* v, uint32_t at) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void lds64(uint32_t* v, uint32_t at) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+}
+
 // many packed rows: tiles of 128 on tcgen05 (attention_kv8_tc.cu)
 cudaError_t launch_attention_kv8_tc(const Kv8Args& A, long long ctas, int hd, cudaStream_t s);
 
-template <auto Kernel>
-cudaError_t launch_kv8(unsigned grid, unsigned threads, int smem, cudaStream_t s, const Kv8Args& A) {
+template <auto Kernel, typename... Args>
+cudaError_t launch_kv8(unsigned grid, unsigned threads, int smem, cudaStream_t s, const Args&... args) {
   if (smem > 48 * 1024) {
     const cudaError_t e = ensure_smem_attr<Kernel>(smem);
     if (e != cudaSuccess) return e;
@@ -105,7 +117,7 @@ cudaError_t launch_kv8(unsigned grid, unsigned threads, int smem, cudaStream_t s
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, Kernel, A);
+  return cudaLaunchKernelEx(&cfg, Kernel, args...);
 }
 
 }  // namespace dllm

@@ -44,6 +44,9 @@ struct ProfScope {
 // cached by (address, shape, box)
 bool tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
                   uint32_t box_rows);
+// one-byte codes [B, N, row_bytes], box (hd bytes of one head, `keys` positions, 1), swizzled
+// over the box's rows (hd 64 or 128 bytes); encoded anew for every launch
+bool tmap_codes(CUtensorMap* m, const void* ptr, int B, int N, int row_bytes, int hd, int keys);
 
 // ----- tcgen05 GEMM -----
 enum EpiKind { EPI_STORE = 0, EPI_RESID = 1, EPI_SWIGLU = 2, EPI_QKV = 3, EPI_LMHEAD = 4 };

@@ -84,4 +84,17 @@ bool tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
   return true;
 }
 
+bool tmap_codes(CUtensorMap* m, const void* ptr, int B, int N, int row_bytes, int hd, int keys) {
+  auto fn = encode_fn();
+  if (!fn || !ptr || (hd != 64 && hd != 128)) return false;
+  cuuint64_t gdim[3] = {(cuuint64_t)row_bytes, (cuuint64_t)N, (cuuint64_t)B};
+  cuuint64_t gstride[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes * N};
+  cuuint32_t box[3] = {(cuuint32_t)hd, (cuuint32_t)keys, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), gdim, gstride, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dllm
