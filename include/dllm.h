@@ -106,6 +106,10 @@ typedef struct {
   const void* w_gate;    /* [ffn, d]               */
   const void* w_up;      /* [ffn, d]               */
   const void* w_down;    /* [d, ffn]               */
+  /* gains of the RMS norm of every query and key head before the rotation
+   * (dllm_qk_norm_rope, eps rms_eps), or both NULL: none */
+  const void* q_norm;    /* [head_dim]             */
+  const void* k_norm;    /* [head_dim]             */
 } dllm_layer_w;
 
 typedef struct {
@@ -140,6 +144,11 @@ typedef struct {
   float* const* att_m;  /* [B, N, n_heads] f32: softmax statistics of each row's attention */
   float* const* att_l;  /* [B, N, n_heads] f32: (reference max and sum, natural log units,
                          * as dllm_attention_stats_bf16), kept up to date by the updates */
+  /* 8-bit caches (policy.kv8_block > 0): k and v point at e4m3 codes of the same shape;
+   * HOST arrays of n_layers device pointers to their scales [B, n_kv_heads,
+   * ceil(N / kv8_block)] f32 (dllm_kv8_write); codes and scales start as zeros */
+  float* const* k_scale;
+  float* const* v_scale;
 } dllm_cache;
 
 typedef struct {
@@ -181,6 +190,11 @@ typedef struct {
   /* Recomputed rows store their query and exact statistics; a dense step     */
   /* stores them for every row.  Layers below score_layer keep no such state.  */
   int attn_update;   /* 0: off                                           */
+  /* K/V caches in 8 bits: positions per scale (16, 32, 64 or 128; DLLM_BF16 */
+  /* models), 0: caches of the model's dtype.  The recomputed rows' K and V  */
+  /* are written with dllm_kv8_write and attended to as the cache holds      */
+  /* them (dllm_attention_kv8); a dense step sets every block's scale anew.  */
+  int kv8_block;
 } dllm_policy;
 
 /* Supported shapes for DLLM_BF16 layer work: d, n_heads*head_dim,

@@ -47,7 +47,7 @@ class ModelCfg(C.Structure):
 
 class LayerW(C.Structure):
     _fields_ = [(n, vp) for n in ("attn_norm", "wq", "wk", "wv", "wo", "ffn_norm", "w_gate",
-                                  "w_up", "w_down")]
+                                  "w_up", "w_down", "q_norm", "k_norm")]
 
 
 class ModelW(C.Structure):
@@ -58,7 +58,8 @@ class ModelW(C.Structure):
 class CacheS(C.Structure):
     _fields_ = [("k", C.POINTER(vp)), ("v", C.POINTER(vp)), ("h_ref", vp), ("conf", vp),
                 ("pred", vp), ("h_ref2", vp), ("ctx", C.POINTER(vp)), ("ffn", C.POINTER(vp)),
-                ("q", C.POINTER(vp)), ("att_m", C.POINTER(vp)), ("att_l", C.POINTER(vp))]
+                ("q", C.POINTER(vp)), ("att_m", C.POINTER(vp)), ("att_l", C.POINTER(vp)),
+                ("k_scale", C.POINTER(vp)), ("v_scale", C.POINTER(vp))]
 
 
 class Policy(C.Structure):
@@ -67,7 +68,8 @@ class Policy(C.Structure):
                 ("gen_start", C.c_int), ("block_len", C.c_int), ("select_from", C.c_int),
                 ("unmask_tau", C.c_float), ("refresh_every", C.c_int),
                 ("refresh_on_block", C.c_int), ("score_layer2", C.c_int), ("k2", C.c_int),
-                ("ffn_gate", C.c_int), ("ffn_tau", C.c_float), ("attn_update", C.c_int)]
+                ("ffn_gate", C.c_int), ("ffn_tau", C.c_float), ("attn_update", C.c_int),
+                ("kv8_block", C.c_int)]
 
 
 class StepIO(C.Structure):
@@ -674,7 +676,8 @@ def cfg_from_shape(s) -> ModelCfg:
 
 def layer_struct(L: Dict[str, object]) -> LayerW:
     return LayerW(*(ptr(L[n]) for n in ("attn_norm", "wq", "wk", "wv", "wo", "ffn_norm",
-                                        "w_gate", "w_up", "w_down")))
+                                        "w_gate", "w_up", "w_down")),
+                  ptr(L.get("q_norm")), ptr(L.get("k_norm")))
 
 
 class Model:
@@ -693,15 +696,20 @@ class Model:
 
 
 class Cache:
-    """Per-layer K/V caches, hidden reference, cached confidence and argmax (torch memory)."""
+    """Per-layer K/V caches, hidden reference, cached confidence and argmax (torch memory).
+    kv8_block > 0: the K/V caches in 8 bits (float8_e4m3fn codes and their scales)."""
 
     def __init__(self, cfg: ModelCfg, B: int, N: int, device="cuda", second_ref: bool = False,
-                 ffn_gate: bool = False, attn_update: bool = False):
-        import torch
+                 ffn_gate: bool = False, attn_update: bool = False, kv8_block: int = 0):
         dt = torch.bfloat16 if cfg.dtype == DLLM_BF16 else torch.float32
         kv = (B, N, cfg.n_kv_heads, cfg.head_dim)
-        self.k = [torch.zeros(kv, dtype=dt, device=device) for _ in range(cfg.n_layers)]
-        self.v = [torch.zeros(kv, dtype=dt, device=device) for _ in range(cfg.n_layers)]
+        self.k_scale = self.v_scale = None
+        if kv8_block:
+            layers = [kv8_cache(*kv, kv8_block, device) for _ in range(cfg.n_layers)]
+            self.k, self.k_scale, self.v, self.v_scale = ([c[i] for c in layers] for i in range(4))
+        else:
+            self.k = [torch.zeros(kv, dtype=dt, device=device) for _ in range(cfg.n_layers)]
+            self.v = [torch.zeros(kv, dtype=dt, device=device) for _ in range(cfg.n_layers)]
         self.h_ref = torch.zeros(B, N, cfg.d, dtype=dt, device=device)
         # reference of the second skip point (policies with score_layer2 > 0)
         self.h_ref2 = torch.zeros(B, N, cfg.d, dtype=dt, device=device) if second_ref else None
@@ -731,18 +739,21 @@ class Cache:
         self._qp = (vp * L)(*[ptr(t) for t in self.q]) if self.q else None
         self._mp = (vp * L)(*[ptr(t) for t in self.att_m]) if self.att_m else None
         self._lp = (vp * L)(*[ptr(t) for t in self.att_l]) if self.att_l else None
+        self._ksp = (vp * L)(*[ptr(t) for t in self.k_scale]) if self.k_scale else None
+        self._vsp = (vp * L)(*[ptr(t) for t in self.v_scale]) if self.v_scale else None
         self.s = CacheS(self._kp, self._vp, ptr(self.h_ref), ptr(self.conf), ptr(self.pred),
-                        ptr(self.h_ref2), self._cp, self._fp, self._qp, self._mp, self._lp)
+                        ptr(self.h_ref2), self._cp, self._fp, self._qp, self._mp, self._lp,
+                        self._ksp, self._vsp)
 
 
 def make_policy(score_layer=0, alpha=0.5, kind=DLLM_SCORE_COS, mode=DLLM_SELECT_TOPK, k=1,
                 tau=0.0, n_unmask=1, gen_start=0, block_len=32, select_from=0, unmask_tau=0.0,
                 refresh_every=0, refresh_on_block=False, score_layer2=0, k2=0, ffn_gate=False,
-                ffn_tau=0.0, attn_update=False) -> Policy:
+                ffn_tau=0.0, attn_update=False, kv8_block=0) -> Policy:
     return Policy(score_layer, float(alpha), kind, mode, k, float(tau), n_unmask, gen_start,
                   block_len, int(select_from), float(unmask_tau), int(refresh_every),
                   int(bool(refresh_on_block)), int(score_layer2), int(k2), int(bool(ffn_gate)),
-                  float(ffn_tau), int(bool(attn_update)))
+                  float(ffn_tau), int(bool(attn_update)), int(kv8_block))
 
 
 def dllm_partial_layer_workspace_size(cfg: ModelCfg, B: int, N: int, k_cap: int) -> int:

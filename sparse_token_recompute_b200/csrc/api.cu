@@ -188,6 +188,8 @@ dllm_status check_layer_w(const dllm_layer_w* w) {
                        w->ffn_norm, w->w_gate, w->w_up, w->w_down};
   for (const void* p : ps)
     if (!aligned(p, 16)) return DLLM_ERR_INVALID_ARG;
+  if ((w->q_norm == nullptr) != (w->k_norm == nullptr)) return DLLM_ERR_INVALID_ARG;
+  if (!aligned(w->q_norm, 16) || !aligned(w->k_norm, 16)) return DLLM_ERR_INVALID_ARG;
   return DLLM_OK;
 }
 
@@ -209,10 +211,13 @@ struct LayerWs {
   float* uraw;
   float* part;  // partial outputs of the key-split attention
   size_t part_bytes;
+  void* kn;     // compact K and V rows on their way into an 8-bit cache
+  void* vn;
 };
 
 // scratch of a layer pass over up to `cap` compact rows
-void layout_layer(Bump& bp, const dllm_model_cfg* c, int B, int N, int cap, LayerWs& w) {
+void layout_layer(Bump& bp, const dllm_model_cfg* c, int B, int N, int cap, LayerWs& w,
+                  bool kv8 = false) {
   const size_t es = esize(c->dtype);
   const int q = c->n_heads * c->head_dim, kv = c->n_kv_heads * c->head_dim;
   w.row_off = bp.take<int>(B + 1);
@@ -236,6 +241,11 @@ void layout_layer(Bump& bp, const dllm_model_cfg* c, int B, int N, int cap, Laye
     w.vraw = bp.take<float>((size_t)cap * kv);
     w.graw = bp.take<float>((size_t)cap * c->ffn);
     w.uraw = bp.take<float>((size_t)cap * c->ffn);
+  }
+  w.kn = w.vn = nullptr;
+  if (kv8) {
+    w.kn = bp.take<char>((size_t)cap * kv * es);
+    w.vn = bp.take<char>((size_t)cap * kv * es);
   }
 }
 
@@ -272,24 +282,42 @@ struct LayerUpd {
   int* seq_off;    // [B + 1] b * N
 };
 
+// One layer's 8-bit cache: the codes are k_cache / v_cache (see dllm_kv8_write)
+struct LayerKv8 {
+  float* k_scale;
+  float* v_scale;
+  int block;
+};
+
 dllm_status layer_forward(const dllm_model_cfg* c, const dllm_layer_w* lw, void* x, int M_cap,
                           const int* M_dev, const LayerWs& w, int B, int N, int k_cap,
                           void* k_cache, void* v_cache, bool use_rope, cudaStream_t s,
-                          const LayerGate* gate = nullptr, const LayerUpd* upd = nullptr) {
+                          const LayerGate* gate = nullptr, const LayerUpd* upd = nullptr,
+                          const LayerKv8* kv8 = nullptr) {
   const int d = c->d, q = c->n_heads * c->head_dim, kv = c->n_kv_heads * c->head_dim;
   const int F = c->ffn, hd = c->head_dim;
   const float2* rope = use_rope ? w.rope : nullptr;
+  // with q/k norms the projections are stored first, then normalised and rotated in place
+  const bool normed = lw->q_norm != nullptr;
+  const Kv8RowMap rows{nullptr, nullptr, w.row_off, w.row_pos, w.row_seq, B, k_cap, N, M_cap, w.status};
   if (M_cap <= 0) return DLLM_OK;
   if (c->dtype == DLLM_BF16) {
     using bf = __nv_bfloat16;
     bf* xb = static_cast<bf*>(x);
     bf* nb = static_cast<bf*>(w.n);
-    if (upd && upd->partial) {  // the recomputed rows' K/V before this layer rewrites them
-      launch_row_words(k_cache, upd->k_old, w.row_pos, w.row_seq, M_dev, M_cap, N, kv * 2, false,
-                       s);
-      launch_row_words(v_cache, upd->v_old, w.row_pos, w.row_seq, M_dev, M_cap, N, kv * 2, false,
-                       s);
-    }
+    uint8_t* k8 = static_cast<uint8_t*>(k_cache);
+    uint8_t* v8 = static_cast<uint8_t*>(v_cache);
+    // the recomputed rows' K/V, as the cache holds them, to compact rows
+    auto read_kv = [&](void* k_out, void* v_out) {
+      if (kv8)
+        return launch_kv8_read(rows, k8, kv8->k_scale, v8, kv8->v_scale, static_cast<bf*>(k_out), kv,
+                               static_cast<bf*>(v_out), kv, c->n_kv_heads, hd, kv8->block, s);
+      launch_row_words(k_cache, k_out, w.row_pos, w.row_seq, M_dev, M_cap, N, kv * 2, false, s);
+      launch_row_words(v_cache, v_out, w.row_pos, w.row_seq, M_dev, M_cap, N, kv * 2, false, s);
+      return cudaSuccess;
+    };
+    // before this layer rewrites them
+    if (upd && upd->partial && read_kv(upd->k_old, upd->v_old) != cudaSuccess) return DLLM_ERR_CUDA;
     launch_rmsnorm<bf>(xb, static_cast<const bf*>(lw->attn_norm), nb, M_dev, M_cap, d,
                        c->rms_eps, s);
     GemmSpec g{};
@@ -308,15 +336,29 @@ dllm_status layer_forward(const dllm_model_cfg* c, const dllm_layer_w* lw, void*
     g.n_seg = 3;
     g.out = static_cast<bf*>(w.q);
     g.ldo = q;
-    g.kc = static_cast<bf*>(k_cache);
-    g.vc = static_cast<bf*>(v_cache);
+    g.kc = static_cast<bf*>(kv8 ? w.kn : k_cache);
+    g.vc = static_cast<bf*>(kv8 ? w.vn : v_cache);
+    g.kv_compact = kv8 != nullptr;
     g.row_pos = w.row_pos;
     g.row_seq = w.row_seq;
     g.Nseq = N;
     g.hd = hd;
-    g.rope = rope;
+    g.rope = normed ? nullptr : rope;
     if (gemm_launch(g, s) != cudaSuccess) return DLLM_ERR_CUDA;
-    if (launch_attention_tc(static_cast<const bf*>(w.q), M_cap,
+    if (normed && launch_qk_norm_rope(rows, w.q, q, g.kc, kv, w.q, q, g.kc, kv, lw->q_norm, lw->k_norm,
+                                      rope, c->n_heads, c->n_kv_heads, hd, c->rms_eps, true, !kv8,
+                                      !kv8, s) != cudaSuccess)
+      return DLLM_ERR_CUDA;
+    if (kv8) {
+      if (launch_kv8_write(rows, static_cast<const bf*>(w.kn), kv, static_cast<const bf*>(w.vn), kv, k8,
+                           kv8->k_scale, v8, kv8->v_scale, c->n_kv_heads, hd, kv8->block,
+                           s) != cudaSuccess ||
+          launch_attention_kv8(rows, static_cast<const bf*>(w.q), k8, kv8->k_scale, v8, kv8->v_scale,
+                               static_cast<bf*>(w.o), nullptr, c->n_heads, c->n_kv_heads, hd,
+                               kv8->block, w.part, w.part_bytes, upd ? upd->m_c : nullptr,
+                               upd ? upd->l_c : nullptr, s) != cudaSuccess)
+        return DLLM_ERR_CUDA;
+    } else if (launch_attention_tc(static_cast<const bf*>(w.q), M_cap,
                                    static_cast<const bf*>(k_cache),
                                    static_cast<const bf*>(v_cache), static_cast<bf*>(w.o),
                                    w.row_off, B, k_cap, N, c->n_heads, c->n_kv_heads, hd,
@@ -336,10 +378,7 @@ dllm_status layer_forward(const dllm_model_cfg* c, const dllm_layer_w* lw, void*
       launch_row_words(upd->l_cache, upd->l_c, w.row_pos, w.row_seq, M_dev, M_cap, N, Hq * 4,
                        true, s);
       if (upd->partial) {
-        launch_row_words(k_cache, upd->k_new, w.row_pos, w.row_seq, M_dev, M_cap, N, kv * 2,
-                         false, s);
-        launch_row_words(v_cache, upd->v_new, w.row_pos, w.row_seq, M_dev, M_cap, N, kv * 2,
-                         false, s);
+        if (read_kv(upd->k_new, upd->v_new) != cudaSuccess) return DLLM_ERR_CUDA;
         launch_mark_rows(w.row_pos, w.row_seq, M_dev, M_cap, B, N, upd->skip, s);
         launch_seq_offsets(B, N, upd->seq_off, s);
         if (launch_attention_update(static_cast<const bf*>(upd->q_cache), B * N,
@@ -435,7 +474,12 @@ dllm_status layer_forward(const dllm_model_cfg* c, const dllm_layer_w* lw, void*
                     s);
     launch_qkv_post_f32(w.qraw, w.kraw, w.vraw, static_cast<float*>(w.q),
                         static_cast<float*>(k_cache), static_cast<float*>(v_cache), w.row_pos,
-                        w.row_seq, M_dev, M_cap, N, c->n_heads, c->n_kv_heads, hd, rope, s);
+                        w.row_seq, M_dev, M_cap, N, c->n_heads, c->n_kv_heads, hd,
+                        normed ? nullptr : rope, s);
+    if (normed && launch_qk_norm_rope(rows, w.q, q, k_cache, kv, w.q, q, k_cache, kv, lw->q_norm,
+                                      lw->k_norm, rope, c->n_heads, c->n_kv_heads, hd, c->rms_eps,
+                                      false, true, true, s) != cudaSuccess)
+      return DLLM_ERR_CUDA;
     launch_attention_f32(static_cast<const float*>(w.q), static_cast<const float*>(k_cache),
                          static_cast<const float*>(v_cache), static_cast<float*>(w.o), w.row_seq,
                          M_dev, M_cap, N, c->n_heads, c->n_kv_heads, hd, s);
@@ -492,7 +536,7 @@ extern "C" const char* dllm_status_string(int st) {
   return "unknown status";
 }
 
-extern "C" int dllm_version(void) { return 100; }
+extern "C" int dllm_version(void) { return 101; }
 
 extern "C" dllm_status dllm_score(const void* h_cur, const void* h_ref, int B, int N, int d,
                                   int dtype, const void* logits, const int32_t* logit_pos, int Mm,
@@ -923,11 +967,11 @@ int k2_cap_of(const dllm_policy* pol, int N) {
 int lm_tiles_for(const dllm_model_cfg* c) { return (c->vocab + 127) / 128; }
 
 void layout_step(Bump& bp, const dllm_model_cfg* c, int B, int N, int k_cap, int k2_cap,
-                 bool gate, bool upd, StepWs& w) {
+                 bool gate, bool upd, bool kv8, StepWs& w) {
   const size_t es = esize(c->dtype);
   const int cap = B * N;  // covers the dense step
   w.status = bp.take<int>(kHeader / sizeof(int));
-  layout_layer(bp, c, B, N, cap, w.L);
+  layout_layer(bp, c, B, N, cap, w.L, kv8);
   w.L.status = w.status;
   w.x = bp.take<char>((size_t)cap * c->d * es);
   w.h_full = bp.take<char>((size_t)cap * c->d * es);
@@ -984,7 +1028,7 @@ extern "C" size_t dllm_step_workspace_size(const dllm_model_cfg* c, int B, int N
   Bump bp(nullptr);
   StepWs w{};
   layout_step(bp, c, B, N, k_cap, k2_cap_of(pol, N), pol->ffn_gate != 0, pol->attn_update != 0,
-              w);
+              pol->kv8_block != 0, w);
   return bp.off;
 }
 
@@ -1063,6 +1107,16 @@ extern "C" dllm_status dllm_step_ex(const dllm_model_cfg* c, const dllm_model_w*
           !aligned(cache->att_m[l], 16) || !aligned(cache->att_l[l], 16))
         return DLLM_ERR_INVALID_ARG;
   }
+  if (pol->kv8_block) {
+    const int kb = pol->kv8_block;
+    if (kb != 16 && kb != 32 && kb != 64 && kb != 128) return DLLM_ERR_INVALID_ARG;
+    if (c->dtype != DLLM_BF16) return DLLM_ERR_UNSUPPORTED_SHAPE;
+    if (!cache->k_scale || !cache->v_scale) return DLLM_ERR_INVALID_ARG;
+    for (int l = 0; l < c->n_layers; ++l)
+      if (!cache->k_scale[l] || !cache->v_scale[l] || !aligned(cache->k_scale[l], 4) ||
+          !aligned(cache->v_scale[l], 4))
+        return DLLM_ERR_INVALID_ARG;
+  }
   const int l2 = pol->score_layer2;
   if (l2 != 0) {
     if (l2 <= pol->score_layer || l2 >= c->n_layers || pol->k2 < 0) return DLLM_ERR_INVALID_ARG;
@@ -1076,7 +1130,8 @@ extern "C" dllm_status dllm_step_ex(const dllm_model_cfg* c, const dllm_model_w*
   const int d = c->d;
   Bump bp(ws);
   StepWs w{};
-  layout_step(bp, c, B, N, k_cap, k2_cap, pol->ffn_gate != 0, pol->attn_update != 0, w);
+  layout_step(bp, c, B, N, k_cap, k2_cap, pol->ffn_gate != 0, pol->attn_update != 0,
+              pol->kv8_block != 0, w);
   LayerWs& L = w.L;
   const bool use_rope = c->rope_theta > 0.f;
   if (use_rope) launch_rope_table(L.rope, N, c->head_dim, c->rope_theta, s);
@@ -1091,6 +1146,12 @@ extern "C" dllm_status dllm_step_ex(const dllm_model_cfg* c, const dllm_model_w*
                    w.g_flag, w.g_list, w.g_inv, w.g_n, w.g_f,
                    io.ffn_rows_out ? io.ffn_rows_out + l : nullptr};
     return &gt;
+  };
+
+  auto kv8_of = [&](int l, LayerKv8& k) -> const LayerKv8* {
+    if (!pol->kv8_block) return nullptr;
+    k = LayerKv8{cache->k_scale[l], cache->v_scale[l], pol->kv8_block};
+    return &k;
   };
 
   // 1. hidden at the score layer: embeddings, then dense layers below it
@@ -1108,8 +1169,9 @@ extern "C" dllm_status dllm_step_ex(const dllm_model_cfg* c, const dllm_model_w*
                                 nullptr, c->vocab, w.status, s);
     for (int l = 0; l < ls; ++l) {
       LayerGate gt;
+      LayerKv8 k8;
       st = layer_forward(c, &mw->layers[l], w.h_full, B * N, M_dev, L, B, N, N, cache->k[l],
-                         cache->v[l], use_rope, s, gate_of(l, true, gt));
+                         cache->v[l], use_rope, s, gate_of(l, true, gt), nullptr, kv8_of(l, k8));
       if (st != DLLM_OK) return st;
     }
     h_src = w.h_full;
@@ -1221,8 +1283,9 @@ extern "C" dllm_status dllm_step_ex(const dllm_model_cfg* c, const dllm_model_w*
                     w.u_kold, w.u_vold, w.u_knew, w.u_vnew, w.u_skip, w.u_off};
       upd = &ut;
     }
+    LayerKv8 k8;
     st = layer_forward(c, &mw->layers[l], xc, cap_c, M_c, L, B, N, rps, cache->k[l],
-                       cache->v[l], use_rope, s, gate_of(l, dense != 0, gt), upd);
+                       cache->v[l], use_rope, s, gate_of(l, dense != 0, gt), upd, kv8_of(l, k8));
     if (st != DLLM_OK) return st;
   }
 

@@ -64,6 +64,7 @@ struct Params {
   const int* row_pos;
   const int* row_seq;
   int Nseq;
+  int kv_compact;  // K/V rows go to the compact row instead of (seq, pos) of the cache
   int q_cols, kv_cols, hd;
   const float2* rope;
   float* lm_part;
@@ -195,16 +196,17 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, int row, bool row
       pos = p.row_pos[row];
       seq = p.row_seq[row];
     }
+    const size_t kv_row = p.kv_compact ? (size_t)row : (size_t)seq * p.Nseq + pos;
     __nv_bfloat16* dst;
     bool rot;
     if (n0 < p.q_cols) {
       dst = p.out + (size_t)row * p.ldo + n0;
       rot = p.rope != nullptr;
     } else if (n0 < p.q_cols + p.kv_cols) {
-      dst = p.kc + ((size_t)seq * p.Nseq + pos) * p.kv_cols + (n0 - p.q_cols);
+      dst = p.kc + kv_row * p.kv_cols + (n0 - p.q_cols);
       rot = p.rope != nullptr;
     } else {
-      dst = p.vc + ((size_t)seq * p.Nseq + pos) * p.kv_cols + (n0 - p.q_cols - p.kv_cols);
+      dst = p.vc + kv_row * p.kv_cols + (n0 - p.q_cols - p.kv_cols);
       rot = false;
     }
     if (!rot) {
@@ -1136,6 +1138,7 @@ cudaError_t gemm_launch(GemmSpec g, cudaStream_t s) {
   p.row_pos = g.row_pos;
   p.row_seq = g.row_seq;
   p.Nseq = g.Nseq;
+  p.kv_compact = g.kv_compact;
   p.q_cols = g.seg_cols[0];
   p.kv_cols = g.n_seg > 1 ? g.seg_cols[1] : 0;
   p.hd = g.hd;

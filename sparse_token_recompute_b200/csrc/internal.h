@@ -72,6 +72,7 @@ struct GemmSpec {
   const int* row_pos;
   const int* row_seq;
   int Nseq;
+  int kv_compact;  // K/V to compact rows of kc/vc instead of the cache rows (row_seq, row_pos)
   int hd;
   const float2* rope;  // [Nseq, hd/2] (cos, sin), null: no rotation
   // LMHEAD partial softmax stats [M_cap, n_tiles] x (max, sum, argmax)
