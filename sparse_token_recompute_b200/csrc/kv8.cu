@@ -2,6 +2,7 @@
 // writing selected rows into the cache, and reading rows back.  All three are
 // bound by HBM (or, for a handful of rows, by the latency of a launch).
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv8.cuh"
@@ -30,101 +31,158 @@ struct NormArgs {
   int k_in_cache, k_out_cache;  // keys at [B, N, Hkv, hd] rows instead of compact ones
 };
 
-// compact row, sequence and position of row `j` of sequence `b` (idx/count) or of
-// compact row `x` (row maps); false: no such row, or a position outside the sequence
-__device__ __forceinline__ bool norm_row(const NormArgs& A, int x, int& r, int& seq, int& pos) {
-  const Kv8Rows& R = A.rows;
-  if (R.row_off) {
-    r = x;
-    if (x >= R.row_off[R.B]) return false;
-    seq = A.row_seq[x];
-    pos = R.row_pos[x];
-    return true;
+struct NormRow {
+  int r, seq, pos;  // compact row (-1: none), sequence, position
+};
+
+// The rows of a call one after the other from row x on: compact row x (row maps), or
+// row x % k_cap of sequence x / k_cap (idx/count).
+struct NormRows {
+  int x, b, j, seq = -1, off = 0, n = 0;
+  __device__ __forceinline__ NormRows(const NormArgs& A, int x0) : x(x0), b(0), j(0) {
+    if (!A.rows.row_off) b = x0 / A.rows.k_cap, j = x0 - b * A.rows.k_cap;
   }
-  seq = x / R.k_cap;
-  const int j = x - seq * R.k_cap;
-  int off, n;
-  kv8_seq_rows(R, seq, off, n);
-  if (j >= n) return false;
-  r = off + j;
-  pos = j;
-  if (R.idx) {
-    const int32_t* l = R.idx + (size_t)seq * R.k_cap;
-    pos = l[j];
-    if ((pos < 0 || pos >= R.N || (j > 0 && l[j - 1] >= pos)) && (threadIdx.x & 31) == 0)
-      raise_status(R.status, DEV_BAD_INDEX);
-  } else if (j >= R.N && (threadIdx.x & 31) == 0) {
-    raise_status(R.status, DEV_BAD_INDEX);
+  __device__ __forceinline__ NormRow next(const NormArgs& A) {
+    const Kv8Rows& R = A.rows;
+    if (R.row_off) {
+      const int i = x++;
+      if (i >= R.row_off[R.B]) return NormRow{-1, 0, 0};
+      return NormRow{i, A.row_seq[i], R.row_pos[i]};
+    }
+    if (j >= R.k_cap) j = 0, ++b;
+    if (b >= R.B) return NormRow{-1, 0, 0};
+    if (b != seq) {
+      seq = b;
+      kv8_seq_rows(R, b, off, n);
+    }
+    const int i = j++;
+    if (i >= n) return NormRow{-1, 0, 0};
+    int pos = i;
+    bool bad;
+    if (R.idx) {
+      const int32_t* l = R.idx + (size_t)b * R.k_cap;
+      pos = l[i];
+      bad = i > 0 && l[i - 1] >= pos;
+    } else {
+      bad = false;
+    }
+    const bool out = (unsigned)pos >= (unsigned)R.N;
+    if ((bad || out) && (threadIdx.x & 31) == 0) raise_status(R.status, DEV_BAD_INDEX);
+    return NormRow{out ? -1 : off + i, b, pos};
   }
-  return pos >= 0 && pos < R.N;
-}
+};
 
 // Head vectors of HD bf16: HD/16 lanes per head, each with 8 elements j.. of the
 // first half and their partners j + HD/2.., so that the rotation is in one lane
 // and a head's sum of squares is 2 or 3 shuffles.  A row's heads (queries, then
-// keys) are spread over `lanes` threads; the sums, the norm and the rotation are
-// fp32, rounded once when stored.
-template <int HD>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormArgs A, int lanes) {
+// keys) are spread over `lanes` threads, each with PASSES of them; a thread takes
+// `rows` rows one after the other, the next one's vectors on their way while it
+// works on the current.  The sums, the norm and the rotation are fp32 (two elements
+// an instruction), rounded once when stored.  Bound by HBM, closely followed by
+// instruction issue: hence addresses and gains that are set up once per thread.
+template <int HD, int PASSES>
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArgs A, int lanes, int rows) {
   griddep_launch_dependents();
   griddep_wait();
+  using bf = __nv_bfloat16;
   constexpr int LPH = HD / 16;
-  const int per_cta = kThreads / lanes;
-  const int x = blockIdx.x * per_cta + threadIdx.x / lanes;
-  const int total = A.rows.row_off ? 0x7fffffff : A.rows.B * A.rows.k_cap;
-  int r, seq, pos;
-  if (x >= total || !norm_row(A, x, r, seq, pos)) return;
+  __shared__ __align__(16) float s_gain[2][HD];
+  for (int i = threadIdx.x; i < 2 * HD; i += kThreads)
+    s_gain[i / HD][i % HD] = bf2f(static_cast<const bf*>(i < HD ? A.q_gain : A.k_gain)[i % HD]);
+  __syncthreads();
   const int l = threadIdx.x % lanes;
   const int e = (l % LPH) * 8;  // first element of this lane in each half
-  float cs[8], sn[8];
+  const int heads = A.Hq + A.Hkv, per_pass = lanes / LPH;
+  const int h0 = blockIdx.y * PASSES * per_pass + l / LPH;  // this lane's first head
+  // the lanes of one head: in each pass all of them have a head or none has
+  const unsigned group = ((1u << LPH) - 1u) << ((threadIdx.x & 31) / LPH * LPH);
+  // per pass: where this lane's elements of row 0 lie and go, and the rows' strides (of
+  // compact rows, or of cache rows where the stride is a whole key row)
+  const char* src[PASSES];
+  char* dst[PASSES];
+  uint32_t ld_in[PASSES], ld_out[PASSES];  // bytes
+  const float4* gain[PASSES];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  if (A.rope) {
-    const float4* t = reinterpret_cast<const float4*>(A.rope + (size_t)pos * (HD / 2) + e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(t + i);
-      cs[2 * i] = v.x, sn[2 * i] = v.y, cs[2 * i + 1] = v.z, sn[2 * i + 1] = v.w;
-    }
-  }
-  const size_t cache_row = (size_t)seq * A.rows.N + pos;
-  using bf = __nv_bfloat16;
-  const bf* qi = static_cast<const bf*>(A.q) + (size_t)r * A.ldq;
-  const bf* ki = static_cast<const bf*>(A.k) + (A.k_in_cache ? cache_row * A.Hkv * HD : (size_t)r * A.ldk);
-  bf* qo = static_cast<bf*>(A.q_out) + (size_t)r * A.ldqo;
-  bf* ko = static_cast<bf*>(A.k_out) + (A.k_out_cache ? cache_row * A.Hkv * HD : (size_t)r * A.ldko);
-  const int heads = A.Hq + A.Hkv;
-  for (int h = l / LPH; h < heads; h += lanes / LPH) {
+  for (int p = 0; p < PASSES; ++p) {
+    const int h = h0 + p * per_pass;
     const bool is_q = h < A.Hq;
     const size_t at = (size_t)(is_q ? h : h - A.Hq) * HD + e;
-    const bf* src = (is_q ? qi : ki) + at;
-    bf* dst = (is_q ? qo : ko) + at;
-    const bf* gain = static_cast<const bf*>(is_q ? A.q_gain : A.k_gain) + e;
-    float a[8], b[8], g[8];
-    unpack8(*reinterpret_cast<const uint4*>(src), a);
-    unpack8(*reinterpret_cast<const uint4*>(src + HD / 2), b);
-    float ss = 0.f;
+    src[p] = static_cast<const char*>(is_q ? A.q : A.k) + at * 2;
+    dst[p] = static_cast<char*>(is_q ? A.q_out : A.k_out) + at * 2;
+    ld_in[p] = 2 * (uint32_t)(is_q ? A.ldq : A.k_in_cache ? A.Hkv * HD : A.ldk);
+    ld_out[p] = 2 * (uint32_t)(is_q ? A.ldqo : A.k_out_cache ? A.Hkv * HD : A.ldko);
+    gain[p] = reinterpret_cast<const float4*>(s_gain[is_q ? 0 : 1] + e);
+  }
+  NormRows list(A, (blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes) * rows);
+  NormRow w = list.next(A);
+  uint4 v[PASSES][2];
+  auto load = [&](const NormRow& t, int p) {
+    const int h = h0 + p * per_pass;
+    if (t.r < 0 || h >= heads) return;
+    // (rows of at least 128 bytes: their numbers fit 32 bits)
+    const uint32_t row = h >= A.Hq && A.k_in_cache ? (uint32_t)t.seq * A.rows.N + t.pos : t.r;
+    const char* at = src[p] + (uint64_t)row * ld_in[p];
+    v[p][0] = *reinterpret_cast<const uint4*>(at);
+    v[p][1] = *reinterpret_cast<const uint4*>(at + HD);
+  };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-    // the lanes of one head: every head of a warp's pass exists or none of its lanes does
-    const unsigned group = ((1u << LPH) - 1u) << ((threadIdx.x & 31) / LPH * LPH);
+  for (int p = 0; p < PASSES; ++p) load(w, p);
+  for (int i = 0; i < rows; ++i) {
+    const NormRow next = i + 1 < rows ? list.next(A) : NormRow{-1, 0, 0};
+    float cs[8], sn[8];
 #pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-    const float rs = rsqrtf(ss * (1.0f / HD) + A.eps);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(gain)), g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = a[i] * rs * g[i];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(gain + HD / 2)), g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = b[i] * rs * g[i];
-    float y[8], z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[i] = a[i] * cs[i] - b[i] * sn[i];
-      z[i] = b[i] * cs[i] + a[i] * sn[i];
+    for (int k = 0; k < 4; ++k) {
+      float4 c = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (A.rope && w.r >= 0)
+        c = __ldg(reinterpret_cast<const float4*>(A.rope + (size_t)w.pos * (HD / 2) + e) + k);
+      cs[2 * k] = c.x, sn[2 * k] = c.y, cs[2 * k + 1] = c.z, sn[2 * k + 1] = c.w;
     }
-    *reinterpret_cast<uint4*>(dst) = pack8(y);
-    *reinterpret_cast<uint4*>(dst + HD / 2) = pack8(z);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int h = h0 + p * per_pass;
+      const uint32_t xa[4] = {v[p][0].x, v[p][0].y, v[p][0].z, v[p][0].w};
+      const uint32_t xb[4] = {v[p][1].x, v[p][1].y, v[p][1].z, v[p][1].w};
+      float a[8], b[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[2 * k] = __uint_as_float(xa[k] << 16), a[2 * k + 1] = __uint_as_float(xa[k] & 0xffff0000u);
+        b[2 * k] = __uint_as_float(xb[k] << 16), b[2 * k + 1] = __uint_as_float(xb[k] & 0xffff0000u);
+      }
+      load(next, p);
+      if (w.r < 0 || h >= heads) continue;
+      float ss = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], ss), s1 = fmaf(b[k], b[k], s1);
+      ss += s1;
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+      const float r = rsqrtf(ss * (1.0f / HD) + A.eps);
+      uint32_t ya[4], yb[4];
+#pragma unroll
+      for (int k = 0; k < 8; k += 4) {
+        const float4 ga = gain[p][k / 4], gb = gain[p][HD / 8 + k / 4];
+        const float fa[4] = {ga.x, ga.y, ga.z, ga.w}, fb[4] = {gb.x, gb.y, gb.z, gb.w};
+        float y[4], z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = a[k + i] * r * fa[i], t = b[k + i] * r * fb[i];
+          y[i] = x * cs[k + i] - t * sn[k + i];
+          z[i] = t * cs[k + i] + x * sn[k + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const __nv_bfloat162 u0 = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+          const __nv_bfloat162 u1 = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
+          ya[k / 2 + i] = *reinterpret_cast<const uint32_t*>(&u0);
+          yb[k / 2 + i] = *reinterpret_cast<const uint32_t*>(&u1);
+        }
+      }
+      const uint32_t row = h >= A.Hq && A.k_out_cache ? (uint32_t)w.seq * A.rows.N + w.pos : w.r;
+      char* to = dst[p] + (uint64_t)row * ld_out[p];
+      *reinterpret_cast<uint4*>(to) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+      *reinterpret_cast<uint4*>(to + HD) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+    }
+    w = next;
   }
 }
 
@@ -133,9 +191,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_f32_kernel(const NormAr
   const int heads = A.Hq + A.Hkv;
   const size_t u = (size_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int x = (int)(u / heads), h = (int)(u % heads);
-  int r, seq, pos;
-  if (!A.rows.row_off && x >= A.rows.B * A.rows.k_cap) return;
-  if (!norm_row(A, x, r, seq, pos)) return;
+  const NormRow w = NormRows(A, x).next(A);
+  if (w.r < 0) return;
+  const int r = w.r, seq = w.seq, pos = w.pos;
   const int lane = threadIdx.x & 31, half = HD / 2;
   const bool is_q = h < A.Hq;
   const size_t cache_row = ((size_t)seq * A.rows.N + pos) * A.Hkv * HD;
@@ -379,48 +437,71 @@ struct ReadArgs {
   int Hkv, hd_log2, blk_log2, nblk;
 };
 
-// `lanes` threads per row, 16 codes of K and of V each per turn
-__global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs A, int lanes) {
+// `lanes` threads per row, 16 codes of K and of V per thread and turn; several rows one
+// after the other, so that the addresses of a row cost little: what is fixed for a
+// thread is its place in the row.  Bound by HBM (a third read, two thirds written).
+__global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs A, int lanes, int rows) {
   griddep_launch_dependents();
   griddep_wait();
   const Kv8Rows& R = A.rows;
-  const int x = blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
-  int r, seq, pos;
-  if (R.row_off) {
-    if (x >= R.row_off[R.B]) return;
-    r = x, seq = A.row_seq[x], pos = R.row_pos[x];
-  } else {
-    if (x >= R.B * R.k_cap) return;
-    seq = x / R.k_cap;
-    const int j = x - seq * R.k_cap;
-    int off, n;
-    kv8_seq_rows(R, seq, off, n);
-    if (j >= n) return;
-    r = off + j;
-    const int32_t* l = R.idx ? R.idx + (size_t)seq * R.k_cap : nullptr;
-    pos = l ? l[j] : j;
-    if ((pos < 0 || pos >= R.N || (l && j > 0 && l[j - 1] >= pos)) && (threadIdx.x & 31) == 0)
-      raise_status(R.status, DEV_BAD_INDEX);
-    if (pos < 0 || pos >= R.N) return;
-  }
+  const int x0 = (blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes) * rows;
   const int vecs = (A.Hkv << A.hd_log2) >> 4;
-  const size_t in = ((size_t)seq * R.N + pos) * vecs;
-  for (int i = threadIdx.x % lanes; i < vecs; i += lanes) {
-    const size_t sc = ((size_t)seq * A.Hkv + ((i << 4) >> A.hd_log2)) * A.nblk + (pos >> A.blk_log2);
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(A.c8[kv]) + in + i);
-      const float s = __ldg(A.scale[kv] + sc);
-      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-      float f[16];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float2 lo = e4m3x2_to_float2(q[t]), hi = e4m3x2_to_float2(q[t] >> 16);
-        f[4 * t] = lo.x * s, f[4 * t + 1] = lo.y * s, f[4 * t + 2] = hi.x * s, f[4 * t + 3] = hi.y * s;
+  int seq = -1, off = 0, n = 0;
+  for (int i = 0; i < rows; ++i) {
+    const int x = x0 + i;
+    int r, pos;
+    if (R.row_off) {
+      if (x >= R.row_off[R.B]) return;
+      r = x, seq = A.row_seq[x], pos = R.row_pos[x];
+    } else {
+      if (x >= R.B * R.k_cap) return;
+      const int b = x / R.k_cap, j = x - b * R.k_cap;
+      if (b != seq) {
+        seq = b;
+        kv8_seq_rows(R, b, off, n);
       }
-      uint4* dst = reinterpret_cast<uint4*>(A.out[kv] + (size_t)r * A.ld[kv] + i * 16);
-      dst[0] = pack8(f);
-      dst[1] = pack8(f + 8);
+      if (j >= n) continue;
+      r = off + j, pos = j;
+      if (R.idx) {
+        const int32_t* l = R.idx + (size_t)b * R.k_cap;
+        pos = l[j];
+        if ((pos < 0 || pos >= R.N || (j > 0 && l[j - 1] >= pos)) && (threadIdx.x & 31) == 0)
+          raise_status(R.status, DEV_BAD_INDEX);
+      } else if (j >= R.N && (threadIdx.x & 31) == 0) {
+        raise_status(R.status, DEV_BAD_INDEX);
+      }
+      if (pos < 0 || pos >= R.N) continue;
+    }
+    const size_t in = ((size_t)seq * R.N + pos) * vecs;
+    const size_t sc = (size_t)seq * A.Hkv * A.nblk + (pos >> A.blk_log2);
+    for (int c = threadIdx.x % lanes; c < vecs; c += lanes) {
+      const int at = ((c << 4) >> A.hd_log2) * A.nblk;
+      uint4 w[2];
+      float s[2];
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        w[kv] = __ldg(reinterpret_cast<const uint4*>(A.c8[kv]) + in + c);
+        s[kv] = __ldg(A.scale[kv] + sc + at);
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t q[4] = {w[kv].x, w[kv].y, w[kv].z, w[kv].w};
+        const f32x2 ss = pair_f32(s[kv], s[kv]);
+        uint32_t y[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t h[2];
+          e4m3x4_to_f16x4(q[t], h[0], h[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+            y[2 * t + k] = bf16_of_pair(mul_pair(pair_f32(f.x, f.y), ss));
+          }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(A.out[kv] + (size_t)r * A.ld[kv]) + 2 * c;
+        dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+      }
     }
   }
 }
@@ -432,9 +513,9 @@ int log2_of(int v) {
 }
 
 template <typename K, typename... Args>
-cudaError_t launch(K kernel, unsigned grid, cudaStream_t s, Args... args) {
+cudaError_t launch(K kernel, dim3 grid, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute la[1];
@@ -469,10 +550,21 @@ cudaError_t launch_qk_norm_rope(const Kv8RowMap& m, const void* q, size_t ldq, c
     qk_norm_rope_f32_kernel<<<(unsigned)((units + 7) / 8), kThreads, 0, s>>>(A, hd);
     return cudaGetLastError();
   }
-  const int lanes = lanes_for((Hq + Hkv) * (hd / 16));
-  const unsigned grid = (unsigned)((cap + kThreads / lanes - 1) / (kThreads / lanes));
-  return hd == 128 ? launch(qk_norm_rope_kernel<128>, grid, s, A, lanes)
-                   : launch(qk_norm_rope_kernel<64>, grid, s, A, lanes);
+  // at most 256 threads per row and 4 heads per thread; more heads: more CTAs
+  const int lph = hd / 16, lanes = lanes_for((Hq + Hkv) * lph);
+  const int need = ((Hq + Hkv) * lph + lanes - 1) / lanes;
+  const int passes = need <= 2 ? need : 4;
+  const int per = kThreads / lanes, chunk = passes * lanes / lph;  // rows and heads per CTA
+  // several rows per thread once the GPU is full (3 CTAs per SM)
+  const int rows = std::max(1, std::min(4, cap / (per * 3 * num_sms())));
+  const dim3 grid((unsigned)((cap + per * rows - 1) / (per * rows)), (unsigned)((Hq + Hkv + chunk - 1) / chunk));
+  auto go = [&](auto hd_c) {
+    constexpr int HD = decltype(hd_c)::value;
+    if (passes == 1) return launch(qk_norm_rope_kernel<HD, 1>, grid, s, A, lanes, rows);
+    if (passes == 2) return launch(qk_norm_rope_kernel<HD, 2>, grid, s, A, lanes, rows);
+    return launch(qk_norm_rope_kernel<HD, 4>, grid, s, A, lanes, rows);
+  };
+  return hd == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
 }
 
 cudaError_t launch_kv8_write(const Kv8RowMap& m, const __nv_bfloat16* k, size_t ldk,
@@ -499,7 +591,9 @@ cudaError_t launch_kv8_read(const Kv8RowMap& m, const uint8_t* k8, const float* 
   ProfScope prof("kv8_read", s);
   const int lanes = lanes_for(Hkv * hd / 16);
   const int per = kThreads / lanes;
-  return launch(kv8_read_kernel, (unsigned)((m.M_cap + per - 1) / per), s, A, lanes);
+  // several rows per CTA once the GPU is full (8 CTAs per SM)
+  const int rows = std::max(1, std::min(4, m.M_cap / (per * 8 * num_sms())));
+  return launch(kv8_read_kernel, (unsigned)((m.M_cap + per * rows - 1) / (per * rows)), s, A, lanes, rows);
 }
 
 }  // namespace dllm

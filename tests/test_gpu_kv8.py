@@ -64,7 +64,8 @@ def norm_ref(x, g, pos, theta, eps, H):
 
 
 @pytest.mark.parametrize("dtype,Hq,Hkv,hd", [("bf16", 28, 4, 128), ("bf16", 32, 32, 128), ("bf16", 6, 2, 64),
-                                             ("bf16", 2, 2, 64), ("f32", 4, 4, 64), ("f32", 3, 1, 10),
+                                             ("bf16", 2, 2, 64), ("bf16", 144, 8, 128), ("bf16", 64, 32, 128),
+                                             ("f32", 4, 4, 64), ("f32", 3, 1, 10),
                                              ("f32", 2, 1, 256)])
 @pytest.mark.parametrize("counts,N", [([1, 0, 3], 17), ([70, 33], 200), ([1], 1)])
 @pytest.mark.parametrize("cache", [False, True])
