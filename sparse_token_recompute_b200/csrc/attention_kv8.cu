@@ -21,6 +21,7 @@
 // so that the keys with the largest weight * scale have the weights near 1, and
 // f16's range is kept however far apart the blocks' scales are.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_kv8.cuh"
 
@@ -400,60 +401,59 @@ __global__ void __launch_bounds__(RW * 32, 3)
 }
 
 // The shares of one output row, in share order: M = max m_s, w_s = l_s 2^(m_s - M),
-// O = sum w_s o_s / sum w_s.  One warp per (row, head); lanes hold the weights of 32
-// shares at a time, and 8 shares' slices are on their way at once (one after the
-// other, 64 shares took 20 us).  An empty share has l = 0 and no slice.
-template <int HD>
+// O = sum w_s o_s / sum w_s.  WPR warps per (row, head), each with up to 8 shares whose
+// slices are on their way at once (one warp for 64 shares took 16 us).  An empty share
+// has l = 0, and what its slice holds is dropped.
+template <int HD, int WPR>
 __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   constexpr int PER = HD / 32;
+  __shared__ float s_acc[WPR > 1 ? 8 : 1][HD + 1];
   griddep_launch_dependents();
   griddep_wait();
-  const size_t u = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t u = ((size_t)blockIdx.x * 8 + warp) / WPR;
+  const int s0 = warp % WPR * 8;
   int off, cnt;
   kv8_seq_rows(A.rows, A.rows.B - 1, off, cnt);
-  if (u >= (size_t)(off + cnt) * A.Hq) return;
+  if (u >= (size_t)(off + cnt) * A.Hq) return;  // (the warps of a row together)
   const size_t stride = (size_t)A.part_rows * A.Hq;
-  float2 ml[kKv8MaxShares / 32];
-  float mx = -INFINITY;
+  auto ml_of = [&](int s) {
+    return s < A.S ? *reinterpret_cast<const float2*>(A.part_ml + (s * stride + u) * 2) : make_float2(0.f, 0.f);
+  };
+  const float2 a = ml_of(lane), b = WPR > 4 ? ml_of(lane + 32) : make_float2(0.f, 0.f);
+  float o[8][PER];
 #pragma unroll
-  for (int i = 0; i < kKv8MaxShares / 32; ++i) {
-    ml[i] = make_float2(-INFINITY, 0.f);
-    if (lane + 32 * i < A.S)
-      ml[i] = *reinterpret_cast<const float2*>(A.part_ml + ((lane + 32 * i) * stride + u) * 2);
-    if (ml[i].y != 0.f) mx = fmaxf(mx, ml[i].x);
+  for (int k = 0; k < 8; ++k) {
+    const float* src = A.part_o + (min(s0 + k, A.S - 1) * stride + u) * HD + lane * PER;
+    if constexpr (PER == 4)
+      *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(src);
+    else
+      *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(src);
   }
-  mx = warp_max(mx);
+  const float mx = warp_max(fmaxf(a.y != 0.f ? a.x : -INFINITY, b.y != 0.f ? b.x : -INFINITY));
+  const float wa = a.y != 0.f ? a.y * exp2_approx(a.x - mx) : 0.f;
+  const float wb = b.y != 0.f ? b.y * exp2_approx(b.x - mx) : 0.f;
   float acc[PER], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll
-  for (int i = 0; i < kKv8MaxShares / 32; ++i) {
-    if (32 * i >= A.S) break;
-    const float mine = ml[i].y == 0.f ? 0.f : ml[i].y * exp2_approx(ml[i].x - mx);
-    for (int s0 = 32 * i; s0 < min(A.S, 32 * i + 32); s0 += 8) {
-      float w[8], o[8][PER];
+  for (int k = 0; k < 8; ++k) {
+    const float w = __shfl_sync(0xffffffffu, s0 < 32 ? wa : wb, (s0 + k) & 31);  // 0 past the last share
+    sum += w;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = __shfl_sync(0xffffffffu, mine, (s0 + k) & 31);
-      // every load is issued (from some share's slice) and what an empty share holds dropped
+    for (int x = 0; x < PER; ++x) acc[x] = fmaf(w, w != 0.f ? o[k][x] : 0.f, acc[x]);
+  }
+  if constexpr (WPR > 1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float* src = A.part_o + (min(s0 + k, A.S - 1) * stride + u) * HD + lane * PER;
-        if constexpr (PER == 4)
-          *reinterpret_cast<float4*>(o[k]) = *reinterpret_cast<const float4*>(src);
-        else
-          *reinterpret_cast<float2*>(o[k]) = *reinterpret_cast<const float2*>(src);
-      }
+    for (int x = 0; x < PER; ++x) s_acc[warp][lane * PER + x] = acc[x];
+    if (lane == 0) s_acc[warp][HD] = sum;
+    __syncthreads();
+    if (warp % WPR != 0) return;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+    for (int w = 1; w < WPR; ++w) {  // in share order
+      sum += s_acc[warp + w][HD];
 #pragma unroll
-        for (int x = 0; x < PER; ++x) o[k][x] = w[k] != 0.f ? o[k][x] : 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sum += w[k];
-#pragma unroll
-        for (int x = 0; x < PER; ++x) acc[x] = fmaf(w[k], o[k][x], acc[x]);
-      }
+      for (int x = 0; x < PER; ++x) acc[x] += s_acc[warp + w][lane * PER + x];
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
@@ -462,8 +462,9 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   for (int i = 0; i < PER; i += 2)
     *reinterpret_cast<__nv_bfloat162*>(dst + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
   if (A.st_m && lane == 0) {
-    normal_stats(mx, sum);
-    A.st_m[u] = mx / kKv8Log2e;
+    float m = mx;
+    normal_stats(m, sum);
+    A.st_m[u] = m / kKv8Log2e;
     A.st_l[u] = sum;
   }
 }
@@ -533,9 +534,14 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   }
   if (e != cudaSuccess || pl.shares == 1) return e;
   ProfScope prof("attention_kv8_merge", s);
-  const unsigned grid = (unsigned)(((size_t)m.M_cap * Hq + 7) / 8);
-  return hd == 128 ? launch_kv8<attn_kv8_merge_kernel<128>>(grid, 256, 0, s, A)
-                   : launch_kv8<attn_kv8_merge_kernel<64>>(grid, 256, 0, s, A);
+  auto merge = [&](auto hd_c) {
+    constexpr int HD = decltype(hd_c)::value;
+    const size_t rows = (size_t)m.M_cap * Hq;
+    if (pl.shares <= 8)
+      return launch_kv8<attn_kv8_merge_kernel<HD, 1>>((unsigned)((rows + 7) / 8), 256, 0, s, A);
+    return launch_kv8<attn_kv8_merge_kernel<HD, 8>>((unsigned)rows, 256, 0, s, A);
+  };
+  return hd == 128 ? merge(std::integral_constant<int, 128>{}) : merge(std::integral_constant<int, 64>{});
 }
 
 }  // namespace dllm

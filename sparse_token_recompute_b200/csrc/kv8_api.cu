@@ -186,7 +186,7 @@ extern "C" dllm_status dllm_attention_kv8(const void* q, const void* k8, const f
   if (!ws || !aligned(ws, 256) || ws_bytes < need) return DLLM_ERR_WORKSPACE;
   const Kv8AttnPlan pl = attention_kv8_plan(B, k_cap, N, n_heads, n_kv_heads, head_dim,
                                             (size_t)B * k_cap, need - kHeader);
-  if (pl.ctas > kMaxGrid || (long long)B * k_cap * n_heads / 8 >= kMaxGrid)
+  if (pl.ctas > kMaxGrid || (long long)B * k_cap * n_heads >= kMaxGrid)
     return DLLM_ERR_UNSUPPORTED_SHAPE;
   using bf = __nv_bfloat16;
   return status_of(launch_attention_kv8(
