@@ -50,13 +50,15 @@ template <int HD>
 struct RowsSmem {
   static constexpr int VB = HD / 8;                     // V bytes per lane and key
   static constexpr int TILE = RW * RK * HD;             // codes of 64 keys
-  static constexpr int STAGES = HD == 128 ? 4 : 6;      // of a K and a V tile each
+  static constexpr int STAGES = HD == 128 ? 3 : 5;      // of a K and a V tile each
   static constexpr int RED = RW * RM * HD * 4;          // outputs of the warps, over the ring
   static constexpr int RING = STAGES * 2 * TILE > RED ? STAGES * 2 * TILE : RED;
-  static constexpr int ML_OFF = RING;
+  static constexpr int Q_OFF = RING;                    // Q fragments, then the rows' units
+  static constexpr int U_OFF = Q_OFF + HD / 16 * 512;
+  static constexpr int ML_OFF = U_OFF + RM * 4;
   static constexpr int BAR_OFF = ML_OFF + RW * RM * 2 * 4;
   static constexpr int TOTAL = BAR_OFF + (2 * STAGES + 1) * 8;
-  static_assert(3 * (TOTAL + 1024) <= 228 * 1024, "three CTAs per SM");
+  static_assert(4 * (TOTAL + 1024) <= 228 * 1024, "four CTAs per SM");
 };
 
 // One CTA = up to 16 packed query rows of one (sequence, kv head) and one share of
@@ -68,13 +70,12 @@ struct RowsSmem {
 // keys.  With so few rows the tensor cores' rate does not matter and the kernel is
 // bound by the codes' way: 2 bytes per key and head_dim element.
 template <int HD>
-__global__ void __launch_bounds__(RW * 32, 3)
+__global__ void __launch_bounds__(RW * 32, 4)
     attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const Kv8Args A) {
   griddep_launch_dependents();
   griddep_wait();
   using L = RowsSmem<HD>;
-  constexpr int KS = HD / 16;    // k-steps of Q K^T
   constexpr int NT = HD / 8;     // n-tiles of P V
   constexpr int KV16 = HD / 64;  // 16-byte pieces of a key row per lane
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -153,13 +154,11 @@ __global__ void __launch_bounds__(RW * 32, 3)
   };
   float2 next = scales_of(0);
 
-  // Q fragments of packed rows g and g + 8: in k-step i of a half of 64 elements, lane
-  // t holds elements 16 t + 4 i .. + 3
-  uint32_t qf[KS][4];
-  float rs[2];  // log2 units per raw score of rows g, g + 8
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = tile * RM + g + 8 * i;
+  // Q fragments of packed rows g (by warp 0) and g + 8 (by warp 1), kept in shared memory
+  // for all warps: in k-step i of a half of 64 elements, lane t has elements 16 t + 4 i .. + 3
+  float* unit = reinterpret_cast<float*>(smem + L::U_OFF);  // log2 units per raw score of a row
+  if (warp < 2) {
+    const int i = warp, r = tile * RM + g + 8 * i;
     const bool there = g + 8 * i < R;
     const size_t row = (size_t)(off + r / A.G) * A.Hq + kvh * A.G + r % A.G;
     uint4 raw[KV16][2];
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(RW * 32, 3)
     const int sh = query_shift(__uint_as_float(mx << 16));
     // in two factors: the shift itself may lie outside the normal floats' exponents
     const float f0 = pow2i(sh / 2), f1 = pow2i(sh - sh / 2);
-    rs[i] = A.scale_log2 * pow2i(-(sh / 2)) * pow2i(-(sh - sh / 2));
+    if (t == 0) unit[g + 8 * i] = A.scale_log2 * pow2i(-(sh / 2)) * pow2i(-(sh - sh / 2));
 #pragma unroll
     for (int p = 0; p < KV16; ++p) {
       float f[16];
@@ -190,11 +189,15 @@ __global__ void __launch_bounds__(RW * 32, 3)
       unpack8(raw[p][1], f + 8);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        qf[p * 4 + e][i] = pack_h2(f[4 * e] * f0 * f1, f[4 * e + 1] * f0 * f1);
-        qf[p * 4 + e][2 + i] = pack_h2(f[4 * e + 2] * f0 * f1, f[4 * e + 3] * f0 * f1);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::Q_OFF + (p * 4 + e) * 512 + lane * 16) + i;
+        dst[0] = pack_h2(f[4 * e] * f0 * f1, f[4 * e + 1] * f0 * f1);
+        dst[2] = pack_h2(f[4 * e + 2] * f0 * f1, f[4 * e + 3] * f0 * f1);
       }
     }
   }
+  __syncthreads();
+  const float rs[2] = {unit[g], unit[g + 8]};
+  const uint32_t q_at = ring + L::Q_OFF + lane * 16;
 
   float o[NT][4];
 #pragma unroll
@@ -245,13 +248,16 @@ __global__ void __launch_bounds__(RW * 32, 3)
 #pragma unroll
         for (int n = 0; n < 2; ++n) lds128(q4[n], base + k_at[n][p]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
+          uint32_t qf[4];
+          lds128(qf, q_at + (p * 4 + e) * 512);
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             uint32_t lo, hi;
             e4m3x4_to_f16x4(q4[n][e], lo, hi);
-            mma_f16(s[n], qf[p * 4 + e], lo, hi);
+            mma_f16(s[n], qf, lo, hi);
           }
+        }
       }
       uint32_t w[4][L::VB / 4];
 #pragma unroll
@@ -485,7 +491,7 @@ Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd,
   const int least = pl.tc ? 128 : 256;  // keys that a share holds at least
   pl.tiles = (int)((packed + rows - 1) / rows);
   const long long units = (long long)B * Hkv * pl.tiles;
-  const long long want = std::max(1LL, (pl.tc ? 2LL : 3LL) * num_sms() / std::max(1LL, units));  // CTAs that share an SM
+  const long long want = std::max(1LL, (pl.tc ? 2LL : 4LL) * num_sms() / std::max(1LL, units));  // CTAs that share an SM
   pl.shares = (int)std::max(1LL, std::min({want, (long long)(keys + least - 1) / least, (long long)kKv8MaxShares}));
   while (pl.shares > 1 && part_floats(pl.shares, M_cap, Hq, hd) * sizeof(float) > part_bytes) --pl.shares;
   pl.ctas = units * pl.shares;
