@@ -87,17 +87,14 @@ __global__ void __launch_bounds__(RW * 32, 4)
   const int tile = u % A.tiles;
   u /= A.tiles;
   const int kvh = u % A.Hkv, b = u / A.Hkv;
+  const int N = A.rows.N;
+  const int want = A.kv_len ? A.kv_len[b] : N;
   int off, cnt;
   kv8_seq_rows(A.rows, b, off, cnt);
   const int R = cnt * A.G - tile * RM;  // packed rows left
   if (R <= 0) return;
-  const int N = A.rows.N;
-  int len = N;
-  if (A.kv_len) {
-    const int want = A.kv_len[b];
-    len = min(max(want, 0), N);
-    if (len != want && threadIdx.x == 0) raise_status(A.rows.status, DEV_BAD_SHAPE);
-  }
+  const int len = min(max(want, 0), N);
+  if (len != want && threadIdx.x == 0) raise_status(A.rows.status, DEV_BAD_SHAPE);
   const int all = (len + RW * RK - 1) / (RW * RK);
   const int per = (all + A.S - 1) / A.S;
   const int t_lo = min(all, share * per);
@@ -109,6 +106,21 @@ __global__ void __launch_bounds__(RW * 32, 4)
   auto empty = [&](int st) { return smem_u32(&bars[L::STAGES + st]); };
   const uint32_t ring = smem_u32(smem);
   int* const status = A.rows.status;
+  // warps 0 and 1 read the packed rows g and g + 8 before the codes' copies fill the memory
+  // system's queues (behind every CTA's first copies they took 3 us)
+  uint4 raw[KV16][2];
+  if (warp < 2) {
+    const int r = tile * RM + g + 8 * warp;
+    const size_t row = (size_t)(off + r / A.G) * A.Hq + kvh * A.G + r % A.G;
+#pragma unroll
+    for (int p = 0; p < KV16; ++p)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        raw[p][w] = make_uint4(0, 0, 0, 0);
+        if (g + 8 * warp < R)
+          raw[p][w] = *(reinterpret_cast<const uint4*>(A.q + row * HD + p * 64 + t * 16) + w);
+      }
+  }
   if (ring & 1023u) {  // the swizzle counts from multiples of 1024
     if (threadIdx.x == 0) raise_status(status, DEV_BAD_SHAPE);
     return;
@@ -158,23 +170,17 @@ __global__ void __launch_bounds__(RW * 32, 4)
   // for all warps: in k-step i of a half of 64 elements, lane t has elements 16 t + 4 i .. + 3
   float* unit = reinterpret_cast<float*>(smem + L::U_OFF);  // log2 units per raw score of a row
   if (warp < 2) {
-    const int i = warp, r = tile * RM + g + 8 * i;
-    const bool there = g + 8 * i < R;
-    const size_t row = (size_t)(off + r / A.G) * A.Hq + kvh * A.G + r % A.G;
-    uint4 raw[KV16][2];
+    const int i = warp;
     uint32_t mx = 0;
 #pragma unroll
-    for (int p = 0; p < KV16; ++p) {
-      const uint4* src = reinterpret_cast<const uint4*>(A.q + row * HD + p * 64 + t * 16);
+    for (int p = 0; p < KV16; ++p)
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        raw[p][w] = there ? src[w] : make_uint4(0, 0, 0, 0);
         mx = __vmaxu2(mx, raw[p][w].x & 0x7fff7fffu);
         mx = __vmaxu2(mx, raw[p][w].y & 0x7fff7fffu);
         mx = __vmaxu2(mx, raw[p][w].z & 0x7fff7fffu);
         mx = __vmaxu2(mx, raw[p][w].w & 0x7fff7fffu);
       }
-    }
     mx = max(mx & 0xffffu, mx >> 16);
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
