@@ -40,7 +40,10 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 
 // ---------------------------------------------------------------- few query rows
 
-// packed query rows per (sequence, kv head) that still run here
+// Packed query rows per (sequence, kv head) that still run here: one tile of RM.  At 1 row
+// and 32 x 1536 keys, 32 heads over 32, 73 us against the tcgen05 kernel's 118; at 20 rows
+// over 8 heads 9.6 against 10.5 (1 x 1536 keys) and 25.2 against 20.5 (1 x 16384); at 64
+// rows 36.9 against 30.3 (16 x 1536) and 316 against 180 (64 x 4096).
 constexpr int kKv8TcRows = 16;
 constexpr int RW = 4;        // warps per CTA
 constexpr int RM = 16;       // packed query rows per CTA
@@ -419,15 +422,15 @@ __global__ void __launch_bounds__(RW * 32, 4)
 template <int HD, int WPR>
 __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   constexpr int PER = HD / 32;
-  __shared__ float s_acc[WPR > 1 ? 8 : 1][HD + 1];
+  __shared__ float s_acc[WPR][HD + 1];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t u = ((size_t)blockIdx.x * 8 + warp) / WPR;
-  const int s0 = warp % WPR * 8;
+  const size_t u = WPR > 1 ? blockIdx.x : (size_t)blockIdx.x * 8 + warp;
+  const int s0 = WPR > 1 ? warp * 8 : 0;
   int off, cnt;
   kv8_seq_rows(A.rows, A.rows.B - 1, off, cnt);
-  if (u >= (size_t)(off + cnt) * A.Hq) return;  // (the warps of a row together)
+  if (u >= (size_t)(off + cnt) * A.Hq) return;  // (a row's warps together)
   const size_t stride = (size_t)A.part_rows * A.Hq;
   auto ml_of = [&](int s) {
     return s < A.S ? *reinterpret_cast<const float2*>(A.part_ml + (s * stride + u) * 2) : make_float2(0.f, 0.f);
@@ -460,12 +463,12 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
     for (int x = 0; x < PER; ++x) s_acc[warp][lane * PER + x] = acc[x];
     if (lane == 0) s_acc[warp][HD] = sum;
     __syncthreads();
-    if (warp % WPR != 0) return;
+    if (warp != 0) return;
 #pragma unroll
     for (int w = 1; w < WPR; ++w) {  // in share order
-      sum += s_acc[warp + w][HD];
+      sum += s_acc[w][HD];
 #pragma unroll
-      for (int x = 0; x < PER; ++x) acc[x] += s_acc[warp + w][lane * PER + x];
+      for (int x = 0; x < PER; ++x) acc[x] += s_acc[w][lane * PER + x];
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
@@ -494,11 +497,19 @@ Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd,
   const int keys = std::max(N, 1);
   pl.tc = packed > kKv8TcRows;
   const int rows = pl.tc ? 128 : RM;
-  const int least = pl.tc ? 128 : 256;  // keys that a share holds at least
   pl.tiles = (int)((packed + rows - 1) / rows);
   const long long units = (long long)B * Hkv * pl.tiles;
-  const long long want = std::max(1LL, (pl.tc ? 2LL : 4LL) * num_sms() / std::max(1LL, units));  // CTAs that share an SM
-  pl.shares = (int)std::max(1LL, std::min({want, (long long)(keys + least - 1) / least, (long long)kKv8MaxShares}));
+  // Shares hold 128 keys or more (64: 16.3 us against 11.9 for 16 rows of 1 x 1536 keys, 32
+  // heads over 8; 256: 13.1).  Of the CTAs with few rows four share an SM; of those with
+  // many, one (20 rows of 4 x 1536 keys: 17.7 us against 20.8 with two), unless that leaves
+  // more than 1024 keys to each (20 rows of 6 x 16384 keys: two 70 us, one 91).
+  auto split = [&](int per_sm) {
+    const long long fill = std::max(1LL, (long long)per_sm * num_sms() / std::max(1LL, units));
+    return std::min({fill, (long long)(keys + 127) / 128, (long long)kKv8MaxShares});
+  };
+  long long shares = split(pl.tc ? 1 : 4);
+  if (pl.tc && keys > shares * 1024) shares = split(2);
+  pl.shares = (int)std::max(1LL, shares);
   while (pl.shares > 1 && part_floats(pl.shares, M_cap, Hq, hd) * sizeof(float) > part_bytes) --pl.shares;
   pl.ctas = units * pl.shares;
   return pl;
@@ -549,9 +560,15 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   auto merge = [&](auto hd_c) {
     constexpr int HD = decltype(hd_c)::value;
     const size_t rows = (size_t)m.M_cap * Hq;
+    auto wide = [&](auto wpr_c) {
+      constexpr int WPR = decltype(wpr_c)::value;
+      return launch_kv8<attn_kv8_merge_kernel<HD, WPR>>((unsigned)rows, WPR * 32, 0, s, A);
+    };
     if (pl.shares <= 8)
       return launch_kv8<attn_kv8_merge_kernel<HD, 1>>((unsigned)((rows + 7) / 8), 256, 0, s, A);
-    return launch_kv8<attn_kv8_merge_kernel<HD, 8>>((unsigned)rows, 256, 0, s, A);
+    if (pl.shares <= 16) return wide(std::integral_constant<int, 2>{});
+    if (pl.shares <= 32) return wide(std::integral_constant<int, 4>{});
+    return wide(std::integral_constant<int, 8>{});
   };
   return hd == 128 ? merge(std::integral_constant<int, 128>{}) : merge(std::integral_constant<int, 64>{});
 }

@@ -4,10 +4,10 @@
 // One CTA = one (sequence, kv head), one tile of 128 packed rows and one share of
 // the keys, 64 keys at a time; two CTAs share an SM, so that one's softmax overlaps
 // the other's products.  Warp roles (288 threads):
-//   warps 0 .. 3  converters: the codes of a K or V tile by cp.async into a small
-//                 ring (each thread reads back what it copied itself), one cvt per
-//                 two codes, and f16 to a ring of slots in the 128-byte-swizzled
-//                 layout that TMA would have written;
+//   warps 0 .. 3  converters, two for the K tiles and two for the V tiles: the codes
+//                 by cp.async into a small ring (each thread reads back what it
+//                 copied itself), one cvt per two codes, and f16 to slots in the
+//                 128-byte-swizzled layout that TMA would have written;
 //   warp 4        TMEM owner and tcgen05.mma issuer;
 //   warps 5 .. 8  softmax, one packed row per thread (its TMEM lane): the thread
 //                 first brings its query row to f16 in shared memory.
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int BT = 128;   // packed rows per tile (= TMEM lanes)
 constexpr int BK = 64;    // keys per tile
-constexpr int NSC = 8;    // tiles whose scales are kept: more than the ring runs ahead
+constexpr int NSC = 8;    // tiles whose scales are kept: more than the converters run ahead
 constexpr int NC = 4;     // converter warps
 constexpr int kThreads = (NC + 1 + 4) * 32;
 constexpr uint32_t kTmemCols = 256;
@@ -47,17 +47,18 @@ struct Smem {
   static constexpr int Q_TILE = BT * HD * 2;
   static constexpr int SLOT = BK * HD * 2;
   static constexpr int RAW = BK * HD;                      // codes of a tile
-  static constexpr int RAWS = 4;
+  static constexpr int RAWS = 2;                           // of K, and of V
   static constexpr int BUDGET = 113 * 1024;                // half of 228 KB, 1 KB reserved
-  static constexpr int FIT = (BUDGET - 1024 - Q_TILE - RAWS * RAW) / SLOT;
-  static constexpr int SLOTS = FIT < 8 ? FIT : 8;
-  static constexpr int RING_OFF = Q_TILE;
-  static constexpr int RAW_OFF = RING_OFF + SLOTS * SLOT;
-  static constexpr int SC_OFF = RAW_OFF + RAWS * RAW;      // [NSC][4] float4
+  // K runs a tile ahead of V: with one V slot less both are released a tile before they
+  // are needed again
+  static constexpr int KS = 2, VS = HD == 128 ? 1 : 2;
+  static constexpr int K_OFF = Q_TILE;
+  static constexpr int V_OFF = K_OFF + KS * SLOT;
+  static constexpr int RAW_OFF = V_OFF + VS * SLOT;        // [K, V][RAWS]
+  static constexpr int SC_OFF = RAW_OFF + 2 * RAWS * RAW;      // [NSC][4] float4
   static constexpr int BAR_OFF = SC_OFF + NSC * 4 * 16;
   static constexpr int TOTAL = BAR_OFF + 48 * 8;
   static_assert(TOTAL <= BUDGET, "shared memory");
-  static_assert(SLOTS >= 3 && SLOTS / 2 + 4 <= NSC, "the scales' ring outruns the tiles'");
 };
 
 // f16 x f16 -> fp32, both operands K-major, M x N tile
@@ -68,7 +69,6 @@ constexpr uint32_t idesc_f16(int M, int N) {
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args A) {
   using L = Smem<HD>;
-  constexpr int NS = L::SLOTS, NR = L::RAWS;
   griddep_launch_dependents();
   griddep_wait();
   int u = blockIdx.x;
@@ -108,22 +108,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   auto pv_done = [&](int j) { return smem_u32(&bars[6 + (j & 1)]); };
   auto par = [](int j) { return (uint32_t)((j >> 1) & 1); };
   auto sc_full = [&](int j) { return smem_u32(&bars[8 + j % NSC]); };
+  // of the slots K0 K1 V0 (V1)
   auto full_at = [&](int i) { return smem_u32(&bars[8 + NSC + i]); };
-  auto empty_at = [&](int i) { return smem_u32(&bars[8 + NSC + NS + i]); };
-  static_assert(8 + NSC + 2 * 8 + 1 <= 48, "barrier area holds 48 words");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&bars[8 + NSC + 2 * NS]);
+  auto empty_at = [&](int i) { return smem_u32(&bars[8 + NSC + 4 + i]); };
+  static_assert(8 + NSC + 2 * 4 + 1 <= 48, "barrier area holds 48 words");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(&bars[8 + NSC + 2 * 4]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* const status = A.rows.status;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sQ = smem_u32(sm);
-  const uint32_t sRing = smem_u32(sm + L::RING_OFF);
-  // the ring's order is the issuer's: K0 K1 V0 K2 V1 ... K(T-1) V(T-2) V(T-1)
   const int live_warps = (min(BT, R) + 31) / 32;  // softmax warps that hold a row
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(full_at(i), NC);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(full_at(i), NC / 2);
       mbar_init(empty_at(i), 1);
     }
     for (int i = 0; i < NSC; ++i) mbar_init(sc_full(i), 1);
@@ -151,41 +150,40 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   if (warp < NC) {
     // ---------------------------------------------------------------- converters
     constexpr int HB = HD / 64;   // 64-element boxes of a row
+    constexpr int NV = 4 * HB;    // 16-byte vectors per thread and tile
     const size_t row_bytes = (size_t)A.Hkv * HD;
     const int key0 = k_lo * BK;
-    const int ring = 2 * T;
-    auto is_v = [&](int n) { return n == ring - 1 || (n > 0 && !(n & 1)); };
-    auto tile_of = [&](int n) { return n == ring - 1 ? T - 1 : (n & 1) ? (n + 1) / 2 : n > 0 ? n / 2 - 1 : 0; };
-    // A thread's vectors of a tile: keys row and row + 8 of this warp's 16, HB boxes each,
-    // 16 codes at 16 (lane & 3).  A warp's copy covers 8 rows of 64 bytes, and the 8 lanes
-    // of a store phase fall on 8 different bank groups.
-    const int row = warp * 16 + (lane >> 2);
-    const size_t first = (((size_t)b * N + key0 + row) * A.Hkv + kvh) * HD + (size_t)(lane & 3) * 16;
+    const bool is_v = warp >= NC / 2;
+    // A thread's vectors of a tile: keys row, row + 8, .. + 24 of this warp's 32, HB boxes
+    // each, 16 codes at 16 (lane & 3).  A warp's copy covers 8 rows of 64 bytes, and the 8
+    // lanes of a store phase fall on 8 different bank groups.
+    const int row = (warp & 1) * 32 + (lane >> 2);
+    const uint8_t* next = (is_v ? A.v8 : A.k8) +
+                          (((size_t)b * N + key0 + row) * A.Hkv + kvh) * HD + (size_t)(lane & 3) * 16;
     const size_t eight = 8 * row_bytes, step = BK * row_bytes;
-    const uint32_t raw = smem_u32(sm + L::RAW_OFF) + threadIdx.x * 16;
-    const uint32_t st0 = sRing + row * 128 + (((lane & 3) * 2) ^ (lane >> 2)) * 16;
-    auto fetch = [&](int n, int stage) {
-      if (n < ring) {
-        const int j = tile_of(n);
-        const uint8_t* src = (is_v(n) ? A.v8 : A.k8) + first + (size_t)j * step;
-        const uint32_t dst = raw + stage * L::RAW;
+    const uint32_t raw = smem_u32(sm + L::RAW_OFF) + (is_v ? L::RAWS * L::RAW : 0) + (threadIdx.x & 63) * 16;
+    const uint32_t st0 = smem_u32(sm + (is_v ? L::V_OFF : L::K_OFF)) + row * 128 +
+                         (((lane & 3) * 2) ^ (lane >> 2)) * 16;
+    auto fetch = [&](int j) {
+      if (j < T) {
+        const uint32_t dst = raw + (j & 1) * L::RAW;
         const int left = len - key0 - j * BK - row;  // keys from this thread's first row on
-        if (left > 8) {
+        if (left > 24) {
 #pragma unroll
-          for (int i = 0; i < 2 * HB; ++i)
-            cp_async16(dst + i * (NC * 32 * 16), src + (i / HB) * eight + i % HB * 64);
+          for (int i = 0; i < NV; ++i) cp_async16(dst + i * 1024, next + (i / HB) * eight + i % HB * 64);
         } else {  // keys past the last one arrive as zeros (copies of 0 bytes from a valid row)
 #pragma unroll
-          for (int i = 0; i < 2 * HB; ++i) {
+          for (int i = 0; i < NV; ++i) {
             const bool there = left > i / HB * 8;
-            cp_async16(dst + i * (NC * 32 * 16), there ? src + (i / HB) * eight + i % HB * 64 : A.k8, there);
+            cp_async16(dst + i * 1024, there ? next + (i / HB) * eight + i % HB * 64 : A.k8, there);
           }
         }
+        next += step;
       }
       cp_commit();
     };
-    // the scales of a K/V tile, per 16 keys: by the first lanes of warp j % 4, read when its
-    // previous turn is done
+    // the scales of a K/V tile, per 16 keys: by the first lanes of K's warp j & 1, read when
+    // its previous turn is done
     const size_t sc0 = ((size_t)b * A.Hkv + kvh) * A.nblk;
     auto fetch_scales = [&](int j) {
       const int key = key0 + j * BK + lane * 16;
@@ -196,37 +194,32 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       }
       return f;
     };
-#pragma unroll
-    for (int n = 0; n < NR - 1; ++n) fetch(n, n);
-    float2 sc = fetch_scales(warp);
-    int stage = 0, at = 0;          // of entry n: raw stage n % NR, slot n % NS
-    uint32_t use = 1;               // parity that its slot's release completes
-    for (int n = 0; n < ring; ++n) {
-      fetch(n + NR - 1, (stage + NR - 1) % NR);
-      if (!is_v(n)) {
-        const int j = tile_of(n);
-        if (warp == j % NC) {
-          if (lane < 4) {
-            float4 f = make_float4(sc.x, 0.f, 0.f, 0.f);
-            if (key0 + j * BK + lane * 16 < len) v_scale_parts(sc.y, f.y, f.z);
-            scales[j % NSC * 4 + lane] = f;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sc_full(j));
-          sc = fetch_scales(j + NC);
+    fetch(0);
+    float2 sc = make_float2(0.f, 0.f);
+    if (!is_v) sc = fetch_scales(warp);
+    for (int j = 0; j < T; ++j) {
+      fetch(j + 1);
+      if (!is_v && warp == (j & 1)) {
+        if (lane < 4) {
+          float4 f = make_float4(sc.x, 0.f, 0.f, 0.f);
+          if (key0 + j * BK + lane * 16 < len) v_scale_parts(sc.y, f.y, f.z);
+          scales[j % NSC * 4 + lane] = f;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_full(j));
+        sc = fetch_scales(j + 2);
       }
-      cp_wait<NR - 1>();
-      if (!mbar_wait(empty_at(at), use, abort_flag, status)) break;
-      const uint32_t dst = st0 + at * L::SLOT;
-      const uint32_t from = raw + stage * L::RAW;
+      cp_wait<1>();
+      const int slot = is_v ? j % L::VS : j % L::KS;
+      const int turn = is_v ? j / L::VS : j / L::KS;
+      const int at = is_v ? L::KS + slot : slot;
+      if (!mbar_wait(empty_at(at), (turn & 1) ^ 1, abort_flag, status)) break;
+      const uint32_t dst = st0 + slot * L::SLOT;
+      const uint32_t from = raw + (j & 1) * L::RAW;
 #pragma unroll
-      for (int i = 0; i < 2 * HB; ++i) {
+      for (int i = 0; i < NV; ++i) {
         uint32_t q[4], h[8];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                     : "r"(from + i * (NC * 32 * 16))
-                     : "memory");
+        lds128(q, from + i * 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k) e4m3x4_to_f16x4(q[k], h[2 * k], h[2 * k + 1]);
         const uint32_t to = dst + i % HB * (BK * 128) + i / HB * 1024;
@@ -240,8 +233,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(full_at(at));
-      if (++stage == NR) stage = 0;
-      if (++at == NS) at = 0, use ^= 1u;
     }
     cp_wait<0>();
   } else if (warp == NC) {
@@ -250,29 +241,30 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       constexpr uint32_t idesc_qk = idesc_f16(BT, BK);
       constexpr uint32_t idesc_pv = idesc_f16(BT, HD) | (1u << 16);  // V read MN-major
       bool ok = true, any = false;
-      int at = 0;        // slot of the next ring entry
-      uint32_t use = 0;  // parity that its fill completes
-      auto take = [&]() -> int {
-        if (!mbar_wait(full_at(at), use, abort_flag, status)) return -1;
+      auto take = [&](int i, int turn) -> bool {
+        if (!mbar_wait(full_at(i), turn & 1, abort_flag, status)) return false;
         tc_fence_after();
-        const int i = at;
-        if (++at == NS) at = 0, use ^= 1u;
-        return i;
+        return true;
       };
       auto give = [&](int i) { tc_commit(empty_at(i)); };
       // operand descriptors: the high words are constant, the low ones count 16 bytes
-      const uint64_t dq = umma_desc_k_sw128(sQ), dk = umma_desc_k_sw128(sRing),
-                     dv = umma_desc_mn_sw128(sRing, BK * 128);
-      auto qk = [&](int j, int i) {
+      const uint64_t dq = umma_desc_k_sw128(sQ), dk = umma_desc_k_sw128(smem_u32(sm + L::K_OFF)),
+                     dv = umma_desc_mn_sw128(smem_u32(sm + L::V_OFF), BK * 128);
+      auto qk = [&](int j) -> bool {
+        const int i = j % L::KS;
+        if (!take(i, j / L::KS)) return false;
         const uint64_t b0 = dk + (uint64_t)(i * (L::SLOT / 16));
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_bf16(tS(j), dq + ((kk >> 2) * (BT * 128) + (kk & 3) * 32) / 16,
                       b0 + ((kk >> 2) * (BK * 128) + (kk & 3) * 32) / 16, idesc_qk, kk > 0 ? 1u : 0u);
         tc_commit(s_full(j));
-        any = true;
+        give(i);
+        return any = true;
       };
-      auto pv = [&](int j, int i) -> bool {
+      auto pv = [&](int j) -> bool {
+        const int i = j % L::VS;
+        if (!take(L::KS + i, j / L::VS)) return false;
         if (!mbar_wait(p_full(j), par(j), abort_flag, status)) return false;
         tc_fence_after();
         const uint64_t b0 = dv + (uint64_t)(i * (L::SLOT / 16));
@@ -281,26 +273,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
           tc_mma_ts(tO, tS(j) + (uint32_t)(kk * 8), b0 + kk * 2048 / 16, idesc_pv,
                     (j > 0 || kk > 0) ? 1u : 0u);
         tc_commit(pv_done(j));
+        give(L::KS + i);
         return true;
       };
       ok = mbar_wait(q_full, 0, abort_flag, status);
-      for (int j = 0; j < 2 && j < T && ok; ++j) {
-        const int k = take();
-        if (!(ok = k >= 0)) break;
-        qk(j, k);
-        give(k);
-      }
-      for (int j = 0; j < T && ok; ++j) {
-        const int v = take();
-        if (!(ok = v >= 0 && pv(j, v))) break;
-        give(v);
-        if (j + 2 < T) {
-          const int k = take();
-          if (!(ok = k >= 0)) break;
-          qk(j + 2, k);
-          give(k);
-        }
-      }
+      tc_fence_after();
+      for (int j = 0; j < 2 && j < T && ok; ++j) ok = qk(j);
+      for (int j = 0; j < T && ok; ++j) ok = pv(j) && (j + 2 >= T || qk(j + 2));
       if (!ok && any) {
         tc_commit(drain_bar);
         mbar_wait_drain(drain_bar, 0, status);
