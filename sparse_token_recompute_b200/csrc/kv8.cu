@@ -255,16 +255,18 @@ __device__ __forceinline__ int warp_lower_bound(const int* __restrict__ l, int n
 }
 
 // One CTA = one block of tokens of one sequence and `hpc` kv heads.  It finds the
-// rows that fall in its block; then each warp takes one (head, K or V) at a time:
-// largest magnitude of the new rows, the block's scale, encode and store.  Tokens
-// that are kept are read only where the scale grew.
+// rows that fall in its block; then 1, 2, 4 or 8 warps take one (head, K or V) at a
+// time, as many as hold its new rows in registers: largest magnitude, the block's
+// scale, encode and store.  Tokens that are kept are read only where the scale grew.
 template <int HD>
-__global__ void __launch_bounds__(kThreads) kv8_write_kernel(const WriteArgs A) {
+__global__ void __launch_bounds__(kThreads, 4) kv8_write_kernel(const WriteArgs A) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int LPR = HD / 8;       // lanes per bf16 row (16 bytes each)
   constexpr int RPL = 32 / LPR;     // rows per load of a warp
-  constexpr int NL = 8;             // loads that stay in registers: RPL * NL rows
+  constexpr int NL = 8;             // loads of a lane at a time: RPL * NL rows of a warp
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps * RPL * NL >= 128, "a block's rows fit the registers");
   constexpr int LPO = HD / 16;      // lanes per row of codes
   constexpr int RPO = 32 / LPO;
   const Kv8Rows& R = A.rows;
@@ -279,30 +281,47 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const WriteArgs A) 
   __shared__ int s_row[128];        // by token of the block: its compact row, or -1
   __shared__ int s_new_row[128];    // the new rows, compacted in token order
   __shared__ uint8_t s_new_tok[128];
-  __shared__ int s_first, s_off, s_n, s_cnt[4];
+  __shared__ int s_cnt[4];
+  __shared__ uint32_t s_top[2][kWarps];
+  // A list of up to SCAN * 256 rows is read whole, all entries at once (those of idx while
+  // the count is on its way); in a longer one the block's first row is searched for.
+  constexpr int SCAN = 4;
+  const int* list = R.row_off || !R.idx ? nullptr : R.idx + (size_t)b * R.k_cap;
+  int pos[SCAN];
+  auto read_list = [&](int rows) {
+#pragma unroll
+    for (int i = 0; i < SCAN; ++i) {
+      const int j = threadIdx.x + i * kThreads;
+      pos[i] = j < rows ? list[j] : -1;
+    }
+  };
+  if (list && R.k_cap <= SCAN * kThreads) read_list(R.k_cap);
   if (threadIdx.x < 128) s_row[threadIdx.x] = -1;
-  if (warp == 0) {
-    int off, n;
-    kv8_seq_rows(R, b, off, n);
-    const int* list = R.row_off ? R.row_pos + off : (R.idx ? R.idx + (size_t)b * R.k_cap : nullptr);
-    const int first = list ? warp_lower_bound(list, n, p0) : min(p0, n);
-    if (lane == 0) s_first = first, s_off = off, s_n = n;
-  }
+  int off, n;
+  kv8_seq_rows(R, b, off, n);
+  if (R.row_off) list = R.row_pos + off;
+  const bool scan = (R.row_off ? n : R.k_cap) <= SCAN * kThreads;
+  if (R.row_off && scan) read_list(n);
   __syncthreads();
-  const int off = s_off, n = s_n, first = s_first;
-  const int* list = R.row_off ? R.row_pos + off : (R.idx ? R.idx + (size_t)b * R.k_cap : nullptr);
+  // (a repeated position: the later row)
+  auto put = [&](int j, int p) {
+    const unsigned t = (unsigned)p - (unsigned)p0;
+    if (j < n && t < (unsigned)tokens) atomicMax(&s_row[t], off + j);
+  };
+  if (!list) {
+    if (threadIdx.x < tokens) put(p0 + threadIdx.x, p0 + threadIdx.x);
+  } else if (scan) {
+#pragma unroll
+    for (int i = 0; i < SCAN; ++i) put(threadIdx.x + i * kThreads, pos[i]);
+  } else {
+    const int j = warp_lower_bound(list, n, p0) + threadIdx.x;
+    if (threadIdx.x < tokens && j < n) put(j, list[j]);
+  }
   if (!R.row_off && R.status && blk == 0 && grp == 0) {  // one CTA per sequence looks the list over
     for (int j = threadIdx.x; j < n; j += kThreads) {
       const int p = list ? list[j] : j;
       if (p < 0 || p >= R.N || (list && j > 0 && list[j - 1] >= p))
         raise_status(R.status, DEV_BAD_INDEX);
-    }
-  }
-  if (threadIdx.x < block) {
-    const int j = first + threadIdx.x;
-    if (j < n) {
-      const int t = (list ? list[j] : j) - p0;
-      if (t >= 0 && t < tokens) atomicMax(&s_row[t], off + j);  // a repeated position: the later row
     }
   }
   __syncthreads();
@@ -321,105 +340,107 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const WriteArgs A) 
   __syncthreads();
 
   const int h0 = grp * A.hpc, h1 = min(A.Hkv, h0 + A.hpc);
+  const int units = 2 * (h1 - h0);
+  int wpu = 1;  // warps per (head, K or V)
+  while (wpu * NL * RPL < n_new) wpu *= 2;
+  const int part = warp & (wpu - 1);
   const int sub = lane / LPR, e = (lane % LPR) * 8;
-  for (int u = warp; u < 2 * (h1 - h0); u += kThreads / 32) {
+  const int k0 = part * RPL + sub, k_step = wpu * RPL;  // this lane's new rows
+  for (int u0 = 0, turn = 0; u0 < units; u0 += kWarps / wpu, turn ^= 1) {
+    const int u = u0 + warp / wpu;
+    const bool active = u < units;
     const int kv = u & 1, h = h0 + (u >> 1);
     const __nv_bfloat16* src = A.x[kv] + (size_t)h * HD + e;
     uint8_t* dst = A.c8[kv] + (((size_t)b * R.N + p0) * A.Hkv + h) * HD;
     float* sp = A.scale[kv] + ((size_t)b * A.Hkv + h) * A.nblk + blk;
-    const float s_old = *sp;
+    const float s_old = active ? *sp : 0.f;
     uint4 v[NL];
     uint32_t mx = 0;  // two running maxima of |x| as bf16 bits
-    auto load = [&](int base) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int k = base + i * RPL + sub;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (k < n_new)
-          v[i] = *reinterpret_cast<const uint4*>(src + (size_t)s_new_row[k] * A.ld[kv]);
-      }
-    };
-    auto magnitude = [&]() {
+    for (int i = 0; i < NL; ++i) {
+      const int k = k0 + i * k_step;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (active && k < n_new) v[i] = *reinterpret_cast<const uint4*>(src + (size_t)s_new_row[k] * A.ld[kv]);
+    }
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        mx = __vmaxu2(mx, v[i].x & 0x7fff7fffu);
-        mx = __vmaxu2(mx, v[i].y & 0x7fff7fffu);
-        mx = __vmaxu2(mx, v[i].z & 0x7fff7fffu);
-        mx = __vmaxu2(mx, v[i].w & 0x7fff7fffu);
-      }
-    };
-    const bool once = n_new <= NL * RPL;
-    for (int base = 0; base < n_new; base += NL * RPL) {
-      load(base);
-      magnitude();
+    for (int i = 0; i < NL; ++i) {
+      mx = __vmaxu2(mx, v[i].x & 0x7fff7fffu);
+      mx = __vmaxu2(mx, v[i].y & 0x7fff7fffu);
+      mx = __vmaxu2(mx, v[i].z & 0x7fff7fffu);
+      mx = __vmaxu2(mx, v[i].w & 0x7fff7fffu);
     }
     uint32_t top = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-    const bool odd = top >= 0x7f80u;  // an infinity or NaN among them: they do not count
+    const bool odd = top >= 0x7f80u;  // an infinity or NaN among this warp's: they do not count
     if (odd) {
       top = 0;
-      for (int k = sub; k < n_new; k += RPL) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + (size_t)s_new_row[k] * A.ld[kv]);
-        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = q[i] & 0x7fffu, hi = (q[i] >> 16) & 0x7fffu;
+      for (int i = 0; i < NL; ++i) {
+        const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t lo = q[t] & 0x7fffu, hi = (q[t] >> 16) & 0x7fffu;
           if (lo < 0x7f80u) top = max(top, lo);
           if (hi < 0x7f80u) top = max(top, hi);
         }
       }
       top = __reduce_max_sync(0xffffffffu, top);
     }
+    if (wpu > 1) {  // (a buffer is written again two turns on, past the next turn's barrier)
+      if (lane == 0) s_top[turn][warp] = top;
+      __syncthreads();
+      for (int w = 0; w < wpu; ++w) top = max(top, s_top[turn][warp - part + w]);
+    }
+    if (!active) continue;
     const float amax = __uint_as_float(top << 16);
     const bool had = s_old >= kKv8MinScale;  // (false for NaN) the block holds rows already
     const bool same = n_new < tokens && had && amax <= kE4m3Max * s_old;
     const float s = same ? s_old : kv8_scale_for(amax);
     const float inv = kv8_inverse(s);
-    auto store = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int k = k0 + i * k_step;
+      if (k >= n_new) continue;
+      float f[8];
+      unpack8(v[i], f);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) f[t] *= inv;
+      if (odd) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (isinf(f[t])) f[t] = __uint_as_float(0x7fffffffu);
+      }
+      uint2 c;
+      c.x = floats_to_e4m3x2(f[0], f[1]) | floats_to_e4m3x2(f[2], f[3]) << 16;
+      c.y = floats_to_e4m3x2(f[4], f[5]) | floats_to_e4m3x2(f[6], f[7]) << 16;
+      *reinterpret_cast<uint2*>(dst + (size_t)s_new_tok[k] * A.Hkv * HD + e) = c;
+    }
+    if (same) continue;
+    if (lane == 0 && part == 0) *sp = s;
+    if (n_new == tokens) continue;
+    // the kept tokens at the new scale (a block without rows yet: zeros)
+    const float f = had ? s_old * inv : 0.f;
+    const int t_step = wpu * RPO;
+    for (int t0 = part * RPO + lane / LPO; t0 < tokens; t0 += NL * t_step) {
+      uint4 w[NL];
+      auto at = [&](int i) {
+        return reinterpret_cast<uint4*>(dst + (size_t)(t0 + i * t_step) * A.Hkv * HD + (lane % LPO) * 16);
+      };
+      auto kept = [&](int i) { return t0 + i * t_step < tokens && s_row[t0 + i * t_step] < 0; };
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const int k = base + i * RPL + sub;
-        if (k >= n_new) continue;
-        float f[8];
-        unpack8(v[i], f);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) f[t] *= inv;
-        if (odd) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (isinf(f[t])) f[t] = __uint_as_float(0x7fffffffu);
-        }
-        uint2 c;
-        c.x = floats_to_e4m3x2(f[0], f[1]) | floats_to_e4m3x2(f[2], f[3]) << 16;
-        c.y = floats_to_e4m3x2(f[4], f[5]) | floats_to_e4m3x2(f[6], f[7]) << 16;
-        *reinterpret_cast<uint2*>(dst + (size_t)s_new_tok[k] * A.Hkv * HD + e) = c;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (had && kept(i)) w[i] = *at(i);
       }
-    };
-    if (once) {
-      store(0);
-    } else {  // more rows than the registers hold: a second look, from the caches
-      for (int base = 0; base < n_new; base += NL * RPL) {
-        load(base);
-        store(base);
-      }
-    }
-    if (!same) {
-      if (lane == 0) *sp = s;
-      // the kept tokens at the new scale (a block without rows yet: zeros)
-      const float f = had ? s_old * inv : 0.f;
-      for (int t = lane / LPO; t < tokens; t += RPO) {
-        if (s_row[t] >= 0) continue;
-        uint4* at = reinterpret_cast<uint4*>(dst + (size_t)t * A.Hkv * HD + (lane % LPO) * 16);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (had) {
-          w = *at;
-          uint32_t* q = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 lo = e4m3x2_to_float2(q[i]), hi = e4m3x2_to_float2(q[i] >> 16);
-            q[i] = floats_to_e4m3x2(lo.x * f, lo.y * f) | floats_to_e4m3x2(hi.x * f, hi.y * f) << 16;
-          }
+      for (int i = 0; i < NL; ++i) {
+        if (!kept(i)) continue;
+        uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 lo = e4m3x2_to_float2(q[k]), hi = e4m3x2_to_float2(q[k] >> 16);
+          q[k] = floats_to_e4m3x2(lo.x * f, lo.y * f) | floats_to_e4m3x2(hi.x * f, hi.y * f) << 16;
         }
-        *at = w;
+        *at(i) = make_uint4(q[0], q[1], q[2], q[3]);
       }
     }
   }
