@@ -259,7 +259,7 @@ __device__ __forceinline__ int warp_lower_bound(const int* __restrict__ l, int n
 // time, as many as hold its new rows in registers: largest magnitude, the block's
 // scale, encode and store.  Tokens that are kept are read only where the scale grew.
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 4) kv8_write_kernel(const WriteArgs A) {
+__global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs A) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int LPR = HD / 8;       // lanes per bf16 row (16 bytes each)
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_write_kernel(const WriteArgs 
 
   __shared__ int s_row[128];        // by token of the block: its compact row, or -1
   __shared__ int s_new_row[128];    // the new rows, compacted in token order
-  __shared__ uint8_t s_new_tok[128];
+  __shared__ uint8_t s_tok[128];    // their tokens, then the tokens that are kept
   __shared__ int s_cnt[4];
   __shared__ uint32_t s_top[2][kWarps];
   // A list of up to SCAN * 256 rows is read whole, all entries at once (those of idx while
@@ -331,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_write_kernel(const WriteArgs 
   __syncthreads();
   const int n_new = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
   if (n_new == 0) return;
-  if (mine >= 0) {
-    int at = __popc(has & ((1u << lane) - 1u));
+  if (threadIdx.x < tokens) {
+    int at = __popc(has & ((1u << lane) - 1u));  // new rows before this token
     for (int w = 0; w < warp; ++w) at += s_cnt[w];
-    s_new_row[at] = mine;
-    s_new_tok[at] = (uint8_t)threadIdx.x;
+    if (mine >= 0) s_new_row[at] = mine;
+    s_tok[mine >= 0 ? at : n_new + (int)threadIdx.x - at] = (uint8_t)threadIdx.x;
   }
   __syncthreads();
 
@@ -396,51 +396,50 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_write_kernel(const WriteArgs 
     const bool same = n_new < tokens && had && amax <= kE4m3Max * s_old;
     const float s = same ? s_old : kv8_scale_for(amax);
     const float inv = kv8_inverse(s);
+    // (powers of two of bf16's range: products that bf16 does not hold exactly are below
+    // 2^-126, and those round to zero codes)
+    const __nv_bfloat162 inv2 = __float2bfloat162_rn(inv);
+    const uint32_t token_bytes = A.Hkv * HD;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int k = k0 + i * k_step;
       if (k >= n_new) continue;
-      float f[8];
-      unpack8(v[i], f);
+      uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t c[4];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) f[t] *= inv;
-      if (odd) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (isinf(f[t])) f[t] = __uint_as_float(0x7fffffffu);
+      for (int t = 0; t < 4; ++t) {
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&q[t]), inv2);
+        uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
+        if (odd) {  // infinities: NaN
+          if ((w & 0x7fffu) == 0x7f80u) w |= 0x7fu;
+          if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x7f0000u;
+        }
+        c[t] = floats_to_e4m3x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
       }
-      uint2 c;
-      c.x = floats_to_e4m3x2(f[0], f[1]) | floats_to_e4m3x2(f[2], f[3]) << 16;
-      c.y = floats_to_e4m3x2(f[4], f[5]) | floats_to_e4m3x2(f[6], f[7]) << 16;
-      *reinterpret_cast<uint2*>(dst + (size_t)s_new_tok[k] * A.Hkv * HD + e) = c;
+      *reinterpret_cast<uint2*>(dst + s_tok[k] * token_bytes + e) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
     if (same) continue;
     if (lane == 0 && part == 0) *sp = s;
-    if (n_new == tokens) continue;
     // the kept tokens at the new scale (a block without rows yet: zeros)
-    const float f = had ? s_old * inv : 0.f;
+    const __half2 f = __float2half2_rn(had ? s_old * inv : 0.f);
     const int t_step = wpu * RPO;
-    for (int t0 = part * RPO + lane / LPO; t0 < tokens; t0 += NL * t_step) {
+    for (int t0 = n_new + part * RPO + lane / LPO; t0 < tokens; t0 += NL * t_step) {
       uint4 w[NL];
-      auto at = [&](int i) {
-        return reinterpret_cast<uint4*>(dst + (size_t)(t0 + i * t_step) * A.Hkv * HD + (lane % LPO) * 16);
-      };
-      auto kept = [&](int i) { return t0 + i * t_step < tokens && s_row[t0 + i * t_step] < 0; };
+      uint32_t at[NL];
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         w[i] = make_uint4(0, 0, 0, 0);
-        if (had && kept(i)) w[i] = *at(i);
+        at[i] = 0;
+        if (t0 + i * t_step >= tokens) continue;
+        at[i] = s_tok[t0 + i * t_step] * token_bytes + (lane % LPO) * 16;
+        if (had) w[i] = *reinterpret_cast<const uint4*>(dst + at[i]);
       }
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        if (!kept(i)) continue;
-        uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = e4m3x2_to_float2(q[k]), hi = e4m3x2_to_float2(q[k] >> 16);
-          q[k] = floats_to_e4m3x2(lo.x * f, lo.y * f) | floats_to_e4m3x2(hi.x * f, hi.y * f) << 16;
-        }
-        *at(i) = make_uint4(q[0], q[1], q[2], q[3]);
+        if (t0 + i * t_step >= tokens) continue;
+        *reinterpret_cast<uint4*>(dst + at[i]) =
+            make_uint4(e4m3x4_scaled(w[i].x, f), e4m3x4_scaled(w[i].y, f), e4m3x4_scaled(w[i].z, f),
+                       e4m3x4_scaled(w[i].w, f));
       }
     }
   }

@@ -55,22 +55,25 @@ __device__ __forceinline__ void kv8_seq_rows(const Kv8Rows& R, int b, int& off, 
   if (c != n && R.status && (threadIdx.x & 31) == 0) raise_status(R.status, DEV_CAPACITY);
 }
 
-// two e4m3 codes (low byte first) as packed f16 (exact; NaN stays NaN)
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(two));
-  return d;
-}
-// four codes: the lower two and the upper two
+// four e4m3 codes (low byte first) as packed f16 (exact; NaN stays NaN)
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(four));
 }
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
-  const uint32_t h = e4m3x2_to_f16x2(two & 0xffffu);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// four codes times a factor 2^-k (0 for k > 24), rounded once: a product that f16 does not
+// hold exactly is below 2^-21, and e4m3 has nothing between 0 and 2^-9
+__device__ __forceinline__ uint32_t e4m3x4_scaled(uint32_t four, __half2 f) {
+  uint32_t h[2];
+  e4m3x4_to_f16x4(four, h[0], h[1]);
+  uint16_t d[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d[i]) : "r"(*reinterpret_cast<const uint32_t*>(&p)));
+  }
+  return d[0] | (uint32_t)d[1] << 16;
 }
 // two floats (|x| <= 448, or NaN) to e4m3 codes, round to nearest even, a in the low byte
 __device__ __forceinline__ uint32_t floats_to_e4m3x2(float a, float b) {
