@@ -182,7 +182,6 @@ def ptr(t) -> Optional[int]:
 
 def _stream(stream):
     if stream is None:
-        import torch
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -190,7 +189,6 @@ def _stream(stream):
 
 
 def _dtype_code(t) -> int:
-    import torch
     if t.dtype == torch.bfloat16:
         return DLLM_BF16
     if t.dtype == torch.float32:
@@ -442,14 +440,20 @@ def _cache_fits(k8, ks, v8, vs, shape, scales, dev):
 
 
 def _rows_fit(t, dtype, width, dev):
-    """The row stride of a 2-D tensor of `width` contiguous elements per row, 0 if it is none."""
+    """Rows and row stride of a 2-D tensor of `width` contiguous elements per row; stride 0 if
+    it is none."""
     sh = t.shape
     if t.dtype is not dtype or len(sh) != 2 or sh[1] != width or t.get_device() != dev:
-        return 0
-    if sh[0] <= 1 and t.is_contiguous():
-        return width
+        return 0, 0
+    if t.is_contiguous():
+        return sh[0], width
     a, b = t.stride()
-    return a if (b == 1 or width == 1) and a >= width else 0
+    return sh[0], a if (b == 1 or width == 1) and a >= width else 0
+
+
+def _cache_rows_fit(t, dtype, shape, dev):
+    """1 if the tensor is a contiguous cache of that shape, else 0."""
+    return int(t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev)
 
 
 def _lists_fit(idx, count, B, rows, dev):
@@ -482,7 +486,7 @@ def _launch(dev: int, fn, args, ws, stream, where: str):
     p, n = (None, 0) if ws is None else (ws.buf.data_ptr(), ws.nbytes)
     if ws is not None and ws.buf.get_device() != dev:
         raise ValueError(f"{where}: the workspace is on {ws.buf.device}")
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, p, n, stream)
     else:
         with torch.cuda.device(dev):
@@ -514,22 +518,24 @@ def dllm_qk_norm_rope(q, k, q_gain, k_gain, rope, q_out, k_out, idx, count, eps:
     if idx is None and count is None:
         raise ValueError("idx or count: the number of sequences is theirs")
     B = (idx if idx is not None else count).shape[0]
-    k_in, k_to = k.dim() == 4, k_out.dim() == 4
+    wq, sk = q.shape[1], k.shape
+    k_in, k_to = len(sk) == 4, k_out.dim() == 4
     if N is None:
-        N = k.shape[1] if k_in else k_out.shape[1] if k_to else rope.shape[0]
-    wq = q.shape[1]
-    wk = k.shape[2] * hd if k_in else k.shape[1]
-    rows = min(q.shape[0], q_out.shape[0], q.shape[0] if k_in else k.shape[0],
-               q.shape[0] if k_to else k_out.shape[0])
-    ldq, ldqo = _rows_fit(q, dt, wq, dev), _rows_fit(q_out, dt, wq, dev)
-    cache = (B, N, wk // hd, hd)
-
-    def kept(t, is_cache):
-        if not is_cache:
-            return _rows_fit(t, dt, wk, dev)
-        return int(t.shape == cache and t.dtype is dt and t.is_contiguous() and t.get_device() == dev)
-
-    ldk, ldko = kept(k, k_in), kept(k_out, k_to)
+        N = sk[1] if k_in else k_out.shape[1] if k_to else rope.shape[0]
+    wk = sk[2] * hd if k_in else sk[1]
+    rows, ldq = _rows_fit(q, dt, wq, dev)
+    n, ldqo = _rows_fit(q_out, dt, wq, dev)
+    rows = n if n < rows else rows
+    if k_in:
+        ldk = _cache_rows_fit(k, dt, (B, N, wk // hd, hd), dev)
+    else:
+        n, ldk = _rows_fit(k, dt, wk, dev)
+        rows = n if n < rows else rows
+    if k_to:
+        ldko = _cache_rows_fit(k_out, dt, (B, N, wk // hd, hd), dev)
+    else:
+        n, ldko = _rows_fit(k_out, dt, wk, dev)
+        rows = n if n < rows else rows
     k_cap = _lists_fit(idx, count, B, rows, dev)
     if not (ldq and ldqo and ldk and ldko and k_cap and dev >= 0 and wq % hd == 0 and wk % hd == 0
             and q_gain.dtype is dt and k_gain.dtype is dt and k_gain.shape == (hd,)
@@ -543,8 +549,8 @@ def dllm_qk_norm_rope(q, k, q_gain, k_gain, rope, q_out, k_out, idx, count, eps:
         if rope is not None and rope.dim() == 3 and rope.shape[0] < N:
             raise ValueError(f"rope: {rope.shape[0]} positions, wanted {N}")
         _bad([("q", q, (dt,), ("rows", wq)), ("q_out", q_out, (dt,), ("rows", wq)),
-              ("k", k, (dt,), cache if k_in else ("rows", wk)),
-              ("k_out", k_out, (dt,), cache if k_to else ("rows", wk)),
+              ("k", k, (dt,), (B, N, wk // hd, hd) if k_in else ("rows", wk)),
+              ("k_out", k_out, (dt,), (B, N, wk // hd, hd) if k_to else ("rows", wk)),
               ("q_gain", q_gain, (dt,), (hd,)), ("k_gain", k_gain, (dt,), (hd,)),
               ("rope", rope, (_F32,), (None, hd // 2, 2))]
              + _list_checks(idx, count, B), dev)
@@ -575,11 +581,12 @@ def _kv8_rows_call(fn, where, k, v, idx, count, k8, k_scale, v8, v_scale, block,
     shape = k8.shape
     B, N, H, hd = shape
     nblk, dev, w = -(-N // max(block, 1)), k8.get_device(), H * hd
-    ldk, ldv = _rows_fit(k, _BF16, w, dev), _rows_fit(v, _BF16, w, dev)
-    rows = min(k.shape[0], v.shape[0])
+    rows, ldk = _rows_fit(k, _BF16, w, dev)
+    n, ldv = _rows_fit(v, _BF16, w, dev)
+    rows = n if n < rows else rows
     k_cap = _lists_fit(idx, count, B, rows, dev)
     if not (ldk and ldv and k_cap and _cache_fits(k8, k_scale, v8, v_scale, shape, (B, H, nblk), dev)):
-        if B and rows < B * (idx.shape[1] if idx is not None else 1):
+        if ldk and ldv and B and rows < B * (idx.shape[1] if idx is not None else 1):
             raise ValueError(f"compact tensors of {rows} rows for {B} sequences")
         bf = (_BF16,)
         _bad([("k", k, bf, ("rows", w)), ("v", v, bf, ("rows", w))]

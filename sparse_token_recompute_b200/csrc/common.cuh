@@ -96,38 +96,6 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-// The same on pairs kept in one 64-bit register from operation to operation: a chain of
-// them then needs no moves between (low: first element).
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair_f32(float lo, float hi) {
-  f32x2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpair_f32(f32x2 a) {
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
-  return d;
-}
-__device__ __forceinline__ f32x2 mul_pair(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 fma_pair(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-// two bf16 of a word, and the other way (rounded to nearest even)
-__device__ __forceinline__ f32x2 pair_of_bf16(uint32_t u) {
-  return pair_f32(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t bf16_of_pair(f32x2 a) {
-  const float2 f = unpair_f32(a);
-  const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
 __device__ __forceinline__ void raise_status(int* status, int bit) {
   if (status) atomicOr(status, bit);
 }

@@ -506,7 +506,6 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs A, in
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t q[4] = {w[kv].x, w[kv].y, w[kv].z, w[kv].w};
-        const f32x2 ss = pair_f32(s[kv], s[kv]);
         uint32_t y[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -515,7 +514,8 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs A, in
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-            y[2 * t + k] = bf16_of_pair(mul_pair(pair_f32(f.x, f.y), ss));
+            const __nv_bfloat162 u = __floats2bfloat162_rn(f.x * s[kv], f.y * s[kv]);
+            y[2 * t + k] = *reinterpret_cast<const uint32_t*>(&u);
           }
         }
         uint4* dst = reinterpret_cast<uint4*>(A.out[kv] + (size_t)r * A.ld[kv]) + 2 * c;
