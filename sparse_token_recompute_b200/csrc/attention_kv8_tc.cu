@@ -20,10 +20,12 @@
 //
 // Bound by shared memory: per 64 keys a CTA moves 128 KB through it (codes in and
 // out 32, f16 tiles 32, Q and K for Q K^T 48, V 16) = 1024 cycles at 128 bytes a
-// cycle, while a tile takes about 1300 of an SM's cycles (32 sequences x 308 rows x
-// 1536 keys, 32 heads: 462 us).  Measured: scores read twice and 128 keys 696 us;
-// codes through registers and L1 540; two row tiles per CTA over the same keys,
-// one CTA per SM, 378 us at 256 rows against 350.
+// cycle.  32 sequences x 308 rows x 1536 keys, 32 heads of 128: over 8 kv heads 347 us
+// (714 TFLOP/s; the kernel over a bf16 cache 380), over 32, where the third of each
+// sequence's tiles holds 52 of 128 rows, 407.  Before, at the latter: scores read twice
+// and 128 keys 696 us; codes through registers and L1 540; K and V converted in turn by
+// the same warps 445 (381 over 8 kv heads).  Two row tiles per CTA over the same keys, one
+// CTA per SM, 378 us at 256 rows against 350; codes by TMA 468 against 441.
 // Every mbarrier wait is bounded; a timeout sets DLLM_DEV_TIMEOUT, drains the MMAs,
 // frees TMEM and returns.
 #include <type_traits>
@@ -55,7 +57,7 @@ struct Smem {
   static constexpr int K_OFF = Q_TILE;
   static constexpr int V_OFF = K_OFF + KS * SLOT;
   static constexpr int RAW_OFF = V_OFF + VS * SLOT;        // [K, V][RAWS]
-  static constexpr int SC_OFF = RAW_OFF + 2 * RAWS * RAW;      // [NSC][4] float4
+  static constexpr int SC_OFF = RAW_OFF + 2 * RAWS * RAW;  // [NSC][4] float4
   static constexpr int BAR_OFF = SC_OFF + NSC * 4 * 16;
   static constexpr int TOTAL = BAR_OFF + 48 * 8;
   static_assert(TOTAL <= BUDGET, "shared memory");

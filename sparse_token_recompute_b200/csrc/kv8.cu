@@ -77,9 +77,11 @@ struct NormRows {
 // and a head's sum of squares is 2 or 3 shuffles.  A row's heads (queries, then
 // keys) are spread over `lanes` threads, each with PASSES of them; a thread takes
 // `rows` rows one after the other, the next one's vectors on their way while it
-// works on the current.  The sums, the norm and the rotation are fp32 (two elements
-// an instruction), rounded once when stored.  Bound by HBM, closely followed by
-// instruction issue: hence addresses and gains that are set up once per thread.
+// works on the current.  The sums, the norm and the rotation are fp32, rounded once
+// when stored.  Bound by HBM, closely followed by instruction issue: hence addresses
+// and gains that are set up once per thread.  32 sequences x up to 308 rows of 32 + 32
+// heads of 128 (279 MB): 66 us, 4.2 TB/s; a copy of the same rows in this shape takes
+// 60.  One row per thread 86 us, up to eight 70, up to four as here.
 template <int HD, int PASSES>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArgs A, int lanes, int rows) {
   griddep_launch_dependents();
@@ -258,6 +260,11 @@ __device__ __forceinline__ int warp_lower_bound(const int* __restrict__ l, int n
 // rows that fall in its block; then 1, 2, 4 or 8 warps take one (head, K or V) at a
 // time, as many as hold its new rows in registers: largest magnitude, the block's
 // scale, encode and store.  Tokens that are kept are read only where the scale grew.
+// Few rows are bound by the way list -> rows -> scale -> kept codes, each a trip to
+// memory, and by instruction issue; many by HBM.  32 sequences, 32 heads of 128, blocks
+// of 64: up to 308 of 1536 rows (206 MB) 51 us, 4.0 TB/s; all rows (1.2 GB) 207 us, 5.8
+// TB/s (one warp with a second look at the rows: 234).  Five CTAs per SM against four:
+// 51 and 207 us against 52 and 210.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs A) {
   griddep_launch_dependents();
@@ -284,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs 
   __shared__ int s_cnt[4];
   __shared__ uint32_t s_top[2][kWarps];
   // A list of up to SCAN * 256 rows is read whole, all entries at once (those of idx while
-  // the count is on its way); in a longer one the block's first row is searched for.
+  // the count is on its way); in a longer one the block's first row is searched for (at 308
+  // rows 55.1 us against 54.9, with twice the CTAs 62.5 against 59.9).
   constexpr int SCAN = 4;
   const int* list = R.row_off || !R.idx ? nullptr : R.idx + (size_t)b * R.k_cap;
   int pos[SCAN];
@@ -459,7 +467,8 @@ struct ReadArgs {
 
 // `lanes` threads per row, 16 codes of K and of V per thread and turn; several rows one
 // after the other, so that the addresses of a row cost little: what is fixed for a
-// thread is its place in the row.  Bound by HBM (a third read, two thirds written).
+// thread is its place in the row.  Bound by HBM (a third read, two thirds written): 32 x
+// 1536 rows of 32 heads of 128 (1.2 GB) 200 us, 6.0 TB/s.
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs A, int lanes, int rows) {
   griddep_launch_dependents();
   griddep_wait();
@@ -575,7 +584,7 @@ cudaError_t launch_qk_norm_rope(const Kv8RowMap& m, const void* q, size_t ldq, c
   const int need = ((Hq + Hkv) * lph + lanes - 1) / lanes;
   const int passes = need <= 2 ? need : 4;
   const int per = kThreads / lanes, chunk = passes * lanes / lph;  // rows and heads per CTA
-  // several rows per thread once the GPU is full (3 CTAs per SM)
+  // several rows per thread once the GPU is full (3 CTAs per SM): 66 us against 86 above
   const int rows = std::max(1, std::min(4, cap / (per * 3 * num_sms())));
   const dim3 grid((unsigned)((cap + per * rows - 1) / (per * rows)), (unsigned)((Hq + Hkv + chunk - 1) / chunk));
   auto go = [&](auto hd_c) {
@@ -592,6 +601,8 @@ cudaError_t launch_kv8_write(const Kv8RowMap& m, const __nv_bfloat16* k, size_t 
                              uint8_t* v8, float* vs, int Hkv, int hd, int block, cudaStream_t s) {
   if (m.M_cap <= 0) return cudaSuccess;
   const int nblk = (m.N + block - 1) / block;
+  // heads per CTA: fewer repeat the list's way, more leave a longer tail (308 of 1536 rows:
+  // 4 heads 60 us, 8 55, 16 57; all rows: 213, 214, 225)
   const int hpc = std::min(Hkv, 8);
   const int groups = (Hkv + hpc - 1) / hpc;
   WriteArgs A{rows_of(m), {k, v}, {ldk, ldv}, {k8, v8}, {ks, vs}, Hkv, log2_of(block), nblk, hpc, groups};
@@ -611,7 +622,8 @@ cudaError_t launch_kv8_read(const Kv8RowMap& m, const uint8_t* k8, const float* 
   ProfScope prof("kv8_read", s);
   const int lanes = lanes_for(Hkv * hd / 16);
   const int per = kThreads / lanes;
-  // several rows per CTA once the GPU is full (8 CTAs per SM)
+  // several rows per CTA once the GPU is full (8 CTAs per SM): at 32 x 1536 rows up to four
+  // take 200 us, one 204, up to eight 206
   const int rows = std::max(1, std::min(4, m.M_cap / (per * 8 * num_sms())));
   return launch(kv8_read_kernel, (unsigned)((m.M_cap + per * rows - 1) / (per * rows)), s, A, lanes, rows);
 }
