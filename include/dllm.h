@@ -532,7 +532,8 @@ dllm_status dllm_attention_bf16_noalloc(const void* q, const void* k_cache, cons
  * whose device status word receives DLLM_DEV_CAPACITY for a count outside
  * [0, k_cap] (clamped) and DLLM_DEV_BAD_INDEX for a list that is not strictly
  * ascending within [0, N): rows at positions outside are skipped, which of
- * the rows with the same position counts is unspecified.  B * k_cap <= 2^30.
+ * the rows with the same position counts is unspecified.  B * k_cap <= 2^30,
+ * N <= 2^30.
  */
 
 /* dllm_rope_table - cos and sin of position p and pair j, angle p *
@@ -600,7 +601,7 @@ dllm_status dllm_kv8_read(const void* k8, const float* k_scale, const void* v8,
  * [B*k_cap, n_heads*head_dim] bf16, rows behind the last sequence's untouched.
  * m, l: both NULL, or [B*k_cap, n_heads] f32 softmax statistics as
  * dllm_attention_stats_bf16 returns them, here with 1 <= l < 2 (-inf and 0
- * without keys).  Any N.
+ * without keys).  B * k_cap * n_heads < 2^31.
  * ws: dllm_attention_kv8_workspace_size() bytes; calls that may overlap need a
  * workspace each.
  */

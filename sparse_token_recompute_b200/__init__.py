@@ -477,6 +477,13 @@ def _list_checks(idx, count, B):
     return [("idx", idx, i32, (B, None)), ("count", count, i32, (B,))]
 
 
+def _stream_context(stream, device):
+    """The stream of a call as torch's current one (None: it is already)."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _launch(dev: int, fn, args, ws, stream, where: str):
     """fn(*args, workspace, bytes, stream) on device `dev`, which is made current for the call."""
     if stream is None:
@@ -644,8 +651,9 @@ def dllm_attention_kv8(q, k8, k_scale, v8, v_scale, o, count, k_cap: int, block:
         _bad([("q", q, bf, (None, wq)), ("o", o, bf, (None, wq)), ("m", m, f32, (None, Hq)),
               ("l", l, f32, (None, Hq))] + _kv8_checks(k8, k_scale, v8, v_scale, B, N, H, hd, nblk)
              + _list_checks(None, count, B) + _list_checks(None, kv_len, B), dev)
-    if ws is None:
-        ws = Workspace(dllm_attention_kv8_workspace_size(B, k_cap, N, Hq, H, hd), k8.device)
+    if ws is None:  # (allocated for, and its status cleared on, the stream of the call)
+        with _stream_context(stream, k8.device):
+            ws = Workspace(dllm_attention_kv8_workspace_size(B, k_cap, N, Hq, H, hd), k8.device)
     _launch(dev, _attn_kv8, (q.data_ptr(), k8.data_ptr(), k_scale.data_ptr(), v8.data_ptr(),
                              v_scale.data_ptr(), o.data_ptr(), ptr(m), ptr(l), ptr(count),
                              ptr(kv_len), B, k_cap, N, Hq, H, hd, block), ws, stream,

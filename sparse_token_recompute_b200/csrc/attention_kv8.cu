@@ -547,7 +547,8 @@ cudaError_t launch_attention_kv8(const Kv8RowMap& m, const __nv_bfloat16* q, con
   A.st_m = st_m, A.st_l = st_l;
   // (no position cached: nothing is copied, and the maps point nowhere)
   CUtensorMap tk{}, tv{};
-  if (m.N > 0 && (!tmap_codes(&tk, k8, m.B, m.N, Hkv * hd, hd, 64) || !tmap_codes(&tv, v8, m.B, m.N, Hkv * hd, hd, 64)))
+  if (!pl.tc && m.N > 0 &&
+      (!tmap_codes(&tk, k8, m.B, m.N, Hkv * hd, hd, 64) || !tmap_codes(&tv, v8, m.B, m.N, Hkv * hd, hd, 64)))
     return cudaErrorInvalidValue;
   cudaError_t e;
   {

@@ -13,6 +13,7 @@ namespace {
 
 constexpr size_t kHeader = 256;                 // device status word at offset 0
 constexpr long long kMaxRows = 1LL << 30;       // B * k_cap
+constexpr int kMaxN = 1 << 30;                  // positions of a sequence
 constexpr long long kMaxGrid = 0x7fffffffLL;
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -26,7 +27,8 @@ inline long long blocks_of(int N, int block) { return ((long long)N + block - 1)
 dllm_status check_rows(const int32_t* idx, const int32_t* count, int k_cap, int B, int N, int Hkv,
                        int hd, const void* ws, size_t ws_bytes) {
   if (B < 0 || N < 0 || k_cap < 1 || Hkv <= 0 || hd <= 0) return DLLM_ERR_INVALID_ARG;
-  if ((long long)B * k_cap > kMaxRows || (long long)Hkv * hd > (1 << 24)) return DLLM_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)B * k_cap > kMaxRows || (long long)Hkv * hd > (1 << 24) || N > kMaxN)
+    return DLLM_ERR_UNSUPPORTED_SHAPE;
   if (!idx && !count && k_cap > N) return DLLM_ERR_CAPACITY;  // more rows than positions
   if (!aligned(idx, 4) || !aligned(count, 4)) return DLLM_ERR_INVALID_ARG;
   if (ws && (ws_bytes < kHeader || !aligned(ws, 256))) return DLLM_ERR_WORKSPACE;
@@ -154,8 +156,9 @@ extern "C" dllm_status dllm_kv8_read(const void* k8, const float* k_scale, const
 
 extern "C" size_t dllm_attention_kv8_workspace_size(int B, int k_cap, int N, int n_heads,
                                                     int n_kv_heads, int head_dim) {
-  if (B <= 0 || k_cap < 1 || N < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads ||
-      head_dim <= 0 || (long long)B * k_cap > kMaxRows)
+  if (B <= 0 || k_cap < 1 || N < 0 || N > kMaxN || n_heads <= 0 || n_kv_heads <= 0 ||
+      n_heads % n_kv_heads || head_dim <= 0 || (long long)B * k_cap > kMaxRows ||
+      (long long)B * k_cap * n_heads >= kMaxGrid)
     return kHeader;
   return kHeader + attention_kv8_part_bytes(B, k_cap, N, n_heads, n_kv_heads, head_dim);
 }
@@ -169,7 +172,8 @@ extern "C" dllm_status dllm_attention_kv8(const void* q, const void* k8, const f
   if (B < 0 || k_cap < 1 || N < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0)
     return DLLM_ERR_INVALID_ARG;
   if (n_heads % n_kv_heads || (head_dim != 64 && head_dim != 128) || !block_ok(block) ||
-      (long long)B * k_cap > kMaxRows || (long long)n_heads * head_dim > (1 << 24))
+      (long long)B * k_cap > kMaxRows || (long long)n_heads * head_dim > (1 << 24) || N > kMaxN ||
+      (long long)B * k_cap * n_heads >= kMaxGrid)
     return DLLM_ERR_UNSUPPORTED_SHAPE;
   if (B == 0) return DLLM_OK;
   if (!q || !o || (m == nullptr) != (l == nullptr)) return DLLM_ERR_INVALID_ARG;
@@ -186,8 +190,7 @@ extern "C" dllm_status dllm_attention_kv8(const void* q, const void* k8, const f
   if (!ws || !aligned(ws, 256) || ws_bytes < need) return DLLM_ERR_WORKSPACE;
   const Kv8AttnPlan pl = attention_kv8_plan(B, k_cap, N, n_heads, n_kv_heads, head_dim,
                                             (size_t)B * k_cap, need - kHeader);
-  if (pl.ctas > kMaxGrid || (long long)B * k_cap * n_heads >= kMaxGrid)
-    return DLLM_ERR_UNSUPPORTED_SHAPE;
+  if (pl.ctas > kMaxGrid) return DLLM_ERR_UNSUPPORTED_SHAPE;
   using bf = __nv_bfloat16;
   return status_of(launch_attention_kv8(
       row_map(nullptr, count, k_cap, B, N, ws), static_cast<const bf*>(q),

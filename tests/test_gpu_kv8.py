@@ -517,3 +517,89 @@ def test_two_captured_chains_replay_beside_each_other(lib, counts):
     chain(lib, a, a["ws"])
     torch.cuda.synchronize()
     assert torch.equal(got, a["o"]) and not torch.equal(got, ref[0])
+
+
+# ------------------------------------------------------------------ other sizes and streams
+
+def test_norm_and_read_of_many_rows(lib):
+    """Rows enough that a thread takes several, across sequences that end inside a run."""
+    B, N, Hq, Hkv, hd, block = 7, 6000, 2, 1, 64, 128
+    idx, cnt, b_of, pos, k = rows_of(B, N, [5000, 1, 0, 4999, 3333, 17, 4998], 5)
+    M, R = len(pos), B * k
+    assert R >= 2 * 8 * 8 * 148   # 8 rows per CTA, 8 CTAs on each SM, twice
+    q, kk = normal((R, Hq * hd), 1).to(BF), normal((R, Hkv * hd), 2).to(BF)
+    g = (1 + 0.1 * normal((hd,), 3)).to(BF)
+    rope = torch.zeros(N, hd // 2, 2, device="cuda")
+    lib.dllm_rope_table(rope, 1e4)
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(kk, 7.0)
+    lib.dllm_qk_norm_rope(q, kk, g, g, rope, qo, ko, idx, cnt, 1e-5)
+    for x, y, H in ((q, qo, Hq), (kk, ko, Hkv)):
+        ref, mag = norm_ref(x[:M], g, pos, 1e4, 1e-5, H)
+        assert np.all(np.abs(f64(y[:M]) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * mag)
+        assert torch.all(y[M:] == 7.0)
+    cache = filled(lib, B, N, Hkv, hd, block, 6)
+    k_out, v_out = torch.full_like(kk, 7.0), torch.full_like(kk, 7.0)
+    lib.dllm_kv8_read(*cache, idx, cnt, k_out, v_out, block)
+    for c, sc, y in ((cache[0], cache[1], k_out), (cache[2], cache[3], v_out)):
+        assert np.array_equal(f64(y[:M]), decoded(c, sc, block)[b_of, pos].reshape(M, -1))
+        assert torch.all(y[M:] == 7.0)
+
+
+@pytest.mark.parametrize("block", [16, 64])
+def test_write_of_long_lists(lib, block):
+    """Lists that are searched rather than read whole, some of them short in a long buffer."""
+    B, N, H, hd = 4, 2777, 2, 64
+    idx, cnt, b_of, pos, k = rows_of(B, N, [1100, 3, 0, 2000], 8)
+    kk, vv = normal((B * k, H * hd), 1, 2.0).to(BF), normal((B * k, H * hd), 2, 2.0).to(BF)
+    cache = filled(lib, B, N, H, hd, block, 9)
+    ref = write_ref(cache, kk, vv, b_of, pos, block)
+    ws = lib.Workspace(256)
+    lib.dllm_kv8_write(kk, vv, idx, cnt, *cache, block, ws=ws)
+    assert ws.device_status() == 0
+    assert_cache(cache, ref, block)
+
+
+def test_kept_rows_at_much_larger_scales(lib):
+    """Every code of a block, kept while its scale grows by 2^1 .. 2^40 (block 0: by nothing)."""
+    N, H, hd, block = 41 * 16, 1, 128, 16
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda")
+    cache = lib.kv8_cache(1, N, H, hd, block)
+    for i in (0, 2):
+        cache[i].view(torch.uint8).copy_(codes.repeat(N * H * hd // 256).view(1, N, H, hd))
+        cache[i + 1].fill_(2.0 ** -5)
+    pos = np.arange(41) * 16 + np.arange(41) % 16
+    idx = torch.from_numpy(pos.astype(np.int32))[None].cuda()
+    x = torch.ones(41, hd, device="cuda") * 448 * 2.0 ** (torch.arange(41, device="cuda") - 5.0)[:, None]
+    kk = x.to(BF)
+    ref = write_ref(cache, kk, -kk, np.zeros(41, int), pos, block)
+    lib.dllm_kv8_write(kk, -kk, idx, None, *cache, block)
+    assert np.array_equal(f64(cache[1])[0, 0], 2.0 ** (np.arange(41) - 5.0))
+    assert_cache(cache, ref, block)
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,hd,block,counts,lens", [
+    (1, 1300, 8, 1, 128, 64, [2], None),               # 11 shares of 16 rows
+    (1, 2600, 4, 1, 64, 32, [3], [2555]),              # 21
+    (2, 9000, 4, 1, 128, 128, [1, 1], [9000, 130]),    # 64, most of the second's empty
+    (1, 1900, 3, 1, 128, 64, [30], None),              # of 128 rows: 15
+    (1, 3700, 2, 1, 64, 16, [50], [3600]),             # 29
+    (2, 70000, 1, 1, 64, 64, [40, 7], [70000, 3]),     # 64, two CTAs per SM if there were fewer
+])
+def test_attention_over_many_shares(lib, B, N, Hq, Hkv, hd, block, counts, lens):
+    q = normal((B * max(counts), Hq * hd), 5).to(BF)
+    check_attention(lib, q, filled(lib, B, N, Hkv, hd, block, 6), block, counts, lens)
+
+
+def test_attention_of_a_given_stream_without_a_workspace(lib):
+    """The workspace that the call makes belongs to the call's stream."""
+    st = chain_state(lib, 101, (1, 1), 4000)
+    for s in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream, torch.cuda.default_stream(), 0):
+        want, got = torch.zeros_like(st["o"]), torch.zeros_like(st["o"])
+        args = (st["cnt"], st["kcap"], st["block"])
+        lib.dllm_attention_kv8(st["q"], *st["cache"], want, *args)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            ws = lib.dllm_attention_kv8(st["q"], *st["cache"], got, *args, stream=s)
+            del ws                                           # reused by the next call, in stream order
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

@@ -146,3 +146,11 @@ def test_the_binding_refuses_what_the_library_would_misread(lib):  # noqa: F811
             n(**kw)
     with pytest.raises(ValueError):
         S.dllm_qk_norm_rope(q, kk, g, g, rope, q, kk, None, None, 1e-5)
+
+
+def test_more_positions_than_the_kernels_count_are_refused(lib):  # noqa: F811
+    import sparse_token_recompute_b200 as S
+    far = (1 << 30) + 1
+    assert _norm(S, N=far) == _write(S, N=far) == _read(S, N=far) == _attn(S, N=far) == 2
+    assert _attn(S, B=1, k_cap=1 << 20, Hq=1 << 11, Hkv=1, hd=64) == 2   # 2^31 rows of heads
+    assert S.dllm_attention_kv8_workspace_size(1, 1, far, 4, 4, 64) == 256
