@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs 
     const int u = u0 + warp / wpu;
     const bool active = u < units;
     const int kv = u & 1, h = h0 + (u >> 1);
-    const __nv_bfloat16* src = A.x[kv] + (size_t)h * HD + e;
+    const char* src = reinterpret_cast<const char*>(A.x[kv] + (size_t)h * HD + e);
+    const uint32_t ld = 2 * (uint32_t)A.ld[kv];  // bytes
     uint8_t* dst = A.c8[kv] + (((size_t)b * R.N + p0) * A.Hkv + h) * HD;
     float* sp = A.scale[kv] + ((size_t)b * A.Hkv + h) * A.nblk + blk;
     const float s_old = active ? *sp : 0.f;
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs 
     for (int i = 0; i < NL; ++i) {
       const int k = k0 + i * k_step;
       v[i] = make_uint4(0, 0, 0, 0);
-      if (active && k < n_new) v[i] = *reinterpret_cast<const uint4*>(src + (size_t)s_new_row[k] * A.ld[kv]);
+      if (active && k < n_new) v[i] = *reinterpret_cast<const uint4*>(src + (uint64_t)(uint32_t)s_new_row[k] * ld);
     }
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -378,17 +379,18 @@ __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs 
       mx = __vmaxu2(mx, v[i].w & 0x7fff7fffu);
     }
     uint32_t top = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-    const bool odd = top >= 0x7f80u;  // an infinity or NaN among this warp's: they do not count
-    if (odd) {
+    if (top >= 0x7f80u) {  // infinities or NaN among this warp's: they do not count, and become NaN
       top = 0;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t* q = reinterpret_cast<uint32_t*>(&v[i]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const uint32_t lo = q[t] & 0x7fffu, hi = (q[t] >> 16) & 0x7fffu;
           if (lo < 0x7f80u) top = max(top, lo);
+          else q[t] |= 0x7fu;
           if (hi < 0x7f80u) top = max(top, hi);
+          else q[t] |= 0x7f0000u;
         }
       }
       top = __reduce_max_sync(0xffffffffu, top);
@@ -417,11 +419,7 @@ __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs 
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&q[t]), inv2);
-        uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
-        if (odd) {  // infinities: NaN
-          if ((w & 0x7fffu) == 0x7f80u) w |= 0x7fu;
-          if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x7f0000u;
-        }
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
         c[t] = floats_to_e4m3x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
       }
       *reinterpret_cast<uint2*>(dst + s_tok[k] * token_bytes + e) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
