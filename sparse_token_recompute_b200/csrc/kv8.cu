@@ -261,10 +261,10 @@ __device__ __forceinline__ int warp_lower_bound(const int* __restrict__ l, int n
 // time, as many as hold its new rows in registers: largest magnitude, the block's
 // scale, encode and store.  Tokens that are kept are read only where the scale grew.
 // Few rows are bound by the way list -> rows -> scale -> kept codes, each a trip to
-// memory, and by instruction issue; many by HBM.  32 sequences, 32 heads of 128, blocks
-// of 64: up to 308 of 1536 rows (206 MB) 51 us, 4.0 TB/s; all rows (1.2 GB) 207 us, 5.8
-// TB/s (one warp with a second look at the rows: 234).  Five CTAs per SM against four:
-// 51 and 207 us against 52 and 210.
+// memory, and by instruction issue (74 % active); many by HBM.  32 sequences, 32 heads of
+// 128, blocks of 64: up to 308 of 1536 rows (206 MB) 48 us, 4.3 TB/s; all rows (1.2 GB)
+// 200 us, 6.0 TB/s (before, one warp with a second look at the rows: 234).  Four CTAs per
+// SM 50 and 201 us, six 52 and 222.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs A) {
   griddep_launch_dependents();
