@@ -79,18 +79,20 @@ struct NormRows {
 // `rows` rows one after the other, the next one's vectors on their way while it
 // works on the current.  The sums, the norm and the rotation are fp32, rounded once
 // when stored.  Bound by HBM, closely followed by instruction issue: hence addresses
-// and gains that are set up once per thread.  32 sequences x up to 308 rows of 32 + 32
-// heads of 128 (279 MB): 66 us, 4.2 TB/s; a copy of the same rows in this shape takes
-// 60.  One row per thread 86 us, up to eight 70, up to four as here.
+// that are set up once per thread, and gains in shared memory as bf16 (fp32 there, with
+// twice the reads: 66 us; in registers, at the cost of a CTA per SM: 75).  32 sequences x
+// up to 308 rows of 32 + 32 heads of 128 (279 MB): 64 us, 4.4 TB/s; a copy of the same
+// rows in this shape takes 60.
 template <int HD, int PASSES>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArgs A, int lanes, int rows) {
   griddep_launch_dependents();
   griddep_wait();
   using bf = __nv_bfloat16;
   constexpr int LPH = HD / 16;
-  __shared__ __align__(16) float s_gain[2][HD];
-  for (int i = threadIdx.x; i < 2 * HD; i += kThreads)
-    s_gain[i / HD][i % HD] = bf2f(static_cast<const bf*>(i < HD ? A.q_gain : A.k_gain)[i % HD]);
+  __shared__ uint4 s_gain[2][HD / 8];  // bf16
+  if (threadIdx.x < HD / 4)
+    s_gain[threadIdx.x / (HD / 8)][threadIdx.x % (HD / 8)] =
+        static_cast<const uint4*>(threadIdx.x < HD / 8 ? A.q_gain : A.k_gain)[threadIdx.x % (HD / 8)];
   __syncthreads();
   const int l = threadIdx.x % lanes;
   const int e = (l % LPH) * 8;  // first element of this lane in each half
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArg
   const char* src[PASSES];
   char* dst[PASSES];
   uint32_t ld_in[PASSES], ld_out[PASSES];  // bytes
-  const float4* gain[PASSES];
+  const uint4* gain[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int h = h0 + p * per_pass;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArg
     dst[p] = static_cast<char*>(is_q ? A.q_out : A.k_out) + at * 2;
     ld_in[p] = 2 * (uint32_t)(is_q ? A.ldq : A.k_in_cache ? A.Hkv * HD : A.ldk);
     ld_out[p] = 2 * (uint32_t)(is_q ? A.ldqo : A.k_out_cache ? A.Hkv * HD : A.ldko);
-    gain[p] = reinterpret_cast<const float4*>(s_gain[is_q ? 0 : 1] + e);
+    gain[p] = s_gain[is_q ? 0 : 1] + e / 8;
   }
   NormRows list(A, (blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes) * rows);
   NormRow w = list.next(A);
@@ -160,10 +162,12 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArg
       for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
       const float r = rsqrtf(ss * (1.0f / HD) + A.eps);
       uint32_t ya[4], yb[4];
+      float ga[8], gb[8];
+      unpack8(gain[p][0], ga);
+      unpack8(gain[p][HD / 16], gb);
 #pragma unroll
       for (int k = 0; k < 8; k += 4) {
-        const float4 ga = gain[p][k / 4], gb = gain[p][HD / 8 + k / 4];
-        const float fa[4] = {ga.x, ga.y, ga.z, ga.w}, fb[4] = {gb.x, gb.y, gb.z, gb.w};
+        const float *fa = ga + k, *fb = gb + k;
         float y[4], z[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -582,7 +586,8 @@ cudaError_t launch_qk_norm_rope(const Kv8RowMap& m, const void* q, size_t ldq, c
   const int need = ((Hq + Hkv) * lph + lanes - 1) / lanes;
   const int passes = need <= 2 ? need : 4;
   const int per = kThreads / lanes, chunk = passes * lanes / lph;  // rows and heads per CTA
-  // several rows per thread once the GPU is full (3 CTAs per SM): 66 us against 86 above
+  // several rows per thread once the GPU is full (3 CTAs per SM): above one took 86 us, up
+  // to four 66, up to eight 70
   const int rows = std::max(1, std::min(4, cap / (per * 3 * num_sms())));
   const dim3 grid((unsigned)((cap + per * rows - 1) / (per * rows)), (unsigned)((Hq + Hkv + chunk - 1) / chunk));
   auto go = [&](auto hd_c) {
