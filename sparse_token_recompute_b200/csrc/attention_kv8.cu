@@ -504,8 +504,9 @@ Kv8AttnPlan attention_kv8_plan(int B, int k_cap, int N, int Hq, int Hkv, int hd,
   const long long units = (long long)B * Hkv * pl.tiles;
   // Shares hold 128 keys or more (64: 16.3 us against 11.9 for 16 rows of 1 x 1536 keys, 32
   // heads over 8; 256: 13.1).  Of the CTAs with few rows four share an SM (1 row of 8 x 16384
-  // keys, 28 heads over 4: 30.8 us; three 34.9, six 35.2); of those with many, one (20 rows of 4 x 1536 keys: 17.7 us against 20.8 with two), unless that leaves
-  // more than 1024 keys to each (20 rows of 6 x 16384 keys: two 70 us, one 91).
+  // keys, 28 heads over 4: 30.8 us; three 34.9, six 35.2); of those with many, one (20 rows
+  // of 4 x 1536 keys: 17.7 us against 20.8 with two), unless that leaves more than 1024 keys
+  // to each (20 rows of 6 x 16384 keys: two 70 us, one 91).
   auto split = [&](int per_sm) {
     const long long fill = std::max(1LL, (long long)per_sm * num_sms() / std::max(1LL, units));
     return std::min({fill, (long long)(keys + 127) / 128, (long long)kKv8MaxShares});
