@@ -212,3 +212,12 @@ def test_step_refuses_an_8_bit_cache_it_cannot_use(lib):
     L.q_norm = c.cache.h_ref.data_ptr()                        # one gain without the other
     with pytest.raises(lib.DllmError):
         go()
+
+
+def test_steps_of_long_sequences(lib):
+    """More rows per sequence than the write reads as one list, from a step's own row maps."""
+    run = Case(lib, shape_of(prompt_len=700, gen_len=600, batch=1, d=256, ratio=0.9), True, 64)
+    assert run.s.k > 1024
+    for t in range(2):
+        out, before = run.step(t == 0)
+        run.check(out, before, t == 0)
