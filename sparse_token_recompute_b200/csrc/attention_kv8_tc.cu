@@ -122,6 +122,68 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   const uint32_t sQ = smem_u32(sm);
   const int live_warps = (min(BT, R) + 31) / 32;  // softmax warps that hold a row
 
+  // the converters' copies and scales: the first ones are on their way while the CTA is set up
+  constexpr int HB = HD / 64;   // 64-element boxes of a row
+  constexpr int NV = 4 * HB;    // 16-byte vectors per thread and tile
+  const size_t row_bytes = (size_t)A.Hkv * HD;
+  const int key0 = k_lo * BK;
+  const bool is_v = warp >= NC / 2;
+  // A thread's vectors of a tile: keys row, row + 8, .. + 24 of this warp's 32, HB boxes
+  // each, 16 codes at 16 (lane & 3).  A warp's copy covers 8 rows of 64 bytes, and the 8
+  // lanes of a store phase fall on 8 different bank groups.
+  const int row = (warp & 1) * 32 + (lane >> 2);
+  const uint8_t* next = (is_v ? A.v8 : A.k8) +
+                        (((size_t)b * N + key0 + row) * A.Hkv + kvh) * HD + (size_t)(lane & 3) * 16;
+  const size_t eight = 8 * row_bytes, step = BK * row_bytes;
+  const uint32_t raw = smem_u32(sm + L::RAW_OFF) + (is_v ? L::RAWS * L::RAW : 0) + (threadIdx.x & 63) * 16;
+  const uint32_t st0 = smem_u32(sm + (is_v ? L::V_OFF : L::K_OFF)) + row * 128 +
+                       (((lane & 3) * 2) ^ (lane >> 2)) * 16;
+  auto fetch = [&](int j) {
+    if (j < T) {
+      const uint32_t dst = raw + (j & 1) * L::RAW;
+      const int left = len - key0 - j * BK - row;  // keys from this thread's first row on
+      if (left > 24) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) cp_async16(dst + i * 1024, next + (i / HB) * eight + i % HB * 64);
+      } else {  // keys past the last one arrive as zeros (copies of 0 bytes from a valid row)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const bool there = left > i / HB * 8;
+          cp_async16(dst + i * 1024, there ? next + (i / HB) * eight + i % HB * 64 : A.k8, there);
+        }
+      }
+      next += step;
+    }
+    cp_commit();
+  };
+  // the scales of a K/V tile, per 16 keys: by the first lanes of K's warp j & 1, read when
+  // its previous turn is done
+  const size_t sc0 = ((size_t)b * A.Hkv + kvh) * A.nblk;
+  auto fetch_scales = [&](int j) {
+    const int key = key0 + j * BK + lane * 16;
+    float2 f = make_float2(0.f, 0.f);
+    if (lane < 4 && j < T && key < len) {
+      f.x = __ldg(A.ks + sc0 + (key >> A.blk_log2));
+      f.y = __ldg(A.vs + sc0 + (key >> A.blk_log2));
+    }
+    return f;
+  };
+  float2 sc = make_float2(0.f, 0.f);
+  if (warp < NC) {
+    fetch(0);
+    if (!is_v) sc = fetch_scales(warp);
+  }
+  // and a softmax thread's query row
+  const int r = (warp & 3) * 32 + lane;  // packed row in the tile (= TMEM lane)
+  const bool there = r < R;
+  const int pr = r0 + r;
+  const size_t at = (size_t)(off + (there ? pr / A.G : 0)) * A.Hq + kvh * A.G + pr % A.G;
+  uint4 q_row[HD / 8];
+  if (warp > NC && T > 0) {
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i)
+      q_row[i] = there ? *(reinterpret_cast<const uint4*>(A.q + at * HD) + i) : make_uint4(0, 0, 0, 0);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(full_at(i), NC / 2);
@@ -151,54 +213,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
 
   if (warp < NC) {
     // ---------------------------------------------------------------- converters
-    constexpr int HB = HD / 64;   // 64-element boxes of a row
-    constexpr int NV = 4 * HB;    // 16-byte vectors per thread and tile
-    const size_t row_bytes = (size_t)A.Hkv * HD;
-    const int key0 = k_lo * BK;
-    const bool is_v = warp >= NC / 2;
-    // A thread's vectors of a tile: keys row, row + 8, .. + 24 of this warp's 32, HB boxes
-    // each, 16 codes at 16 (lane & 3).  A warp's copy covers 8 rows of 64 bytes, and the 8
-    // lanes of a store phase fall on 8 different bank groups.
-    const int row = (warp & 1) * 32 + (lane >> 2);
-    const uint8_t* next = (is_v ? A.v8 : A.k8) +
-                          (((size_t)b * N + key0 + row) * A.Hkv + kvh) * HD + (size_t)(lane & 3) * 16;
-    const size_t eight = 8 * row_bytes, step = BK * row_bytes;
-    const uint32_t raw = smem_u32(sm + L::RAW_OFF) + (is_v ? L::RAWS * L::RAW : 0) + (threadIdx.x & 63) * 16;
-    const uint32_t st0 = smem_u32(sm + (is_v ? L::V_OFF : L::K_OFF)) + row * 128 +
-                         (((lane & 3) * 2) ^ (lane >> 2)) * 16;
-    auto fetch = [&](int j) {
-      if (j < T) {
-        const uint32_t dst = raw + (j & 1) * L::RAW;
-        const int left = len - key0 - j * BK - row;  // keys from this thread's first row on
-        if (left > 24) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) cp_async16(dst + i * 1024, next + (i / HB) * eight + i % HB * 64);
-        } else {  // keys past the last one arrive as zeros (copies of 0 bytes from a valid row)
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const bool there = left > i / HB * 8;
-            cp_async16(dst + i * 1024, there ? next + (i / HB) * eight + i % HB * 64 : A.k8, there);
-          }
-        }
-        next += step;
-      }
-      cp_commit();
-    };
-    // the scales of a K/V tile, per 16 keys: by the first lanes of K's warp j & 1, read when
-    // its previous turn is done
-    const size_t sc0 = ((size_t)b * A.Hkv + kvh) * A.nblk;
-    auto fetch_scales = [&](int j) {
-      const int key = key0 + j * BK + lane * 16;
-      float2 f = make_float2(0.f, 0.f);
-      if (lane < 4 && j < T && key < len) {
-        f.x = __ldg(A.ks + sc0 + (key >> A.blk_log2));
-        f.y = __ldg(A.vs + sc0 + (key >> A.blk_log2));
-      }
-      return f;
-    };
-    fetch(0);
-    float2 sc = make_float2(0.f, 0.f);
-    if (!is_v) sc = fetch_scales(warp);
     for (int j = 0; j < T; ++j) {
       fetch(j + 1);
       if (!is_v && warp == (j & 1)) {
@@ -214,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       cp_wait<1>();
       const int slot = is_v ? j % L::VS : j % L::KS;
       const int turn = is_v ? j / L::VS : j / L::KS;
-      const int at = is_v ? L::KS + slot : slot;
-      if (!mbar_wait(empty_at(at), (turn & 1) ^ 1, abort_flag, status)) break;
+      const int bar = is_v ? L::KS + slot : slot;
+      if (!mbar_wait(empty_at(bar), (turn & 1) ^ 1, abort_flag, status)) break;
       const uint32_t dst = st0 + slot * L::SLOT;
       const uint32_t from = raw + (j & 1) * L::RAW;
 #pragma unroll
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       // generic stores before the tensor core's reads
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(full_at(at));
+      if (lane == 0) mbar_arrive(full_at(bar));
     }
     cp_wait<0>();
   } else if (warp == NC) {
@@ -290,22 +304,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   } else {
     // ------------------------------------------------------------------ softmax
     const int quad = warp & 3;
-    const int r = quad * 32 + lane;  // packed row in the tile (= TMEM lane)
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const bool there = r < R;
-    const int pr = r0 + r;
-    const size_t at = (size_t)(off + (there ? pr / A.G : 0)) * A.Hq + kvh * A.G + pr % A.G;
     float rs = 0.f;  // log2 units per raw score
     if (T > 0) {
-      uint4 raw[HD / 8];
       uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
-        raw[i] = there ? *(reinterpret_cast<const uint4*>(A.q + at * HD) + i) : make_uint4(0, 0, 0, 0);
-        mx = __vmaxu2(mx, raw[i].x & 0x7fff7fffu);
-        mx = __vmaxu2(mx, raw[i].y & 0x7fff7fffu);
-        mx = __vmaxu2(mx, raw[i].z & 0x7fff7fffu);
-        mx = __vmaxu2(mx, raw[i].w & 0x7fff7fffu);
+        mx = __vmaxu2(mx, q_row[i].x & 0x7fff7fffu);
+        mx = __vmaxu2(mx, q_row[i].y & 0x7fff7fffu);
+        mx = __vmaxu2(mx, q_row[i].z & 0x7fff7fffu);
+        mx = __vmaxu2(mx, q_row[i].w & 0x7fff7fffu);
       }
       const int sh = query_shift(__uint_as_float(max(mx & 0xffffu, mx >> 16) << 16));
       const float f0 = pow2i(sh / 2), f1 = pow2i(sh - sh / 2);
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
         float f[8];
-        unpack8(raw[i], f);
+        unpack8(q_row[i], f);
         uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = pack_h2(f[2 * k] * f0 * f1, f[2 * k + 1] * f0 * f1);
