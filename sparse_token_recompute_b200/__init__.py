@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import json
+import operator
 import os
 from typing import Dict, List, Optional, Sequence
 
@@ -131,17 +132,26 @@ _attn_upd = _sig("dllm_attention_update_bf16", _i, [vp, vp, vp, vp, vp, _i, _i, 
                                                     vp, _i, _i, _i, _i, vp, _sz, vp])
 _attn = _sig("dllm_attention_bf16", _i, [vp, vp, vp, vp, vp, _i, _i, _i, _i, _i, _i, vp, _sz,
                                          vp])
+
+
+class _Int:
+    """A C int argument of the calls whose host time matters: ctypes passes a Python int as it
+    is, without the c_int instance (about 0.1 us each) that the type itself makes."""
+    from_param = operator.index
+
+
 _rope_table = _sig("dllm_rope_table", _i, [vp, _i, _i, _f, vp])
-_qk_norm = _sig("dllm_qk_norm_rope", _i, [vp, _i, vp, _i, _i, vp, vp, vp, vp, _i, vp, _i, _i, vp,
-                                          vp, _i, _i, _i, _i, _i, _i, _f, _i, vp, _sz, vp])
+_n = _Int
+_qk_norm = _sig("dllm_qk_norm_rope", _i, [vp, _n, vp, _n, _n, vp, vp, vp, vp, _n, vp, _n, _n, vp,
+                                          vp, _n, _n, _n, _n, _n, _n, _f, _n, vp, _sz, vp])
 _kv8_scales = _sig("dllm_kv8_scale_count", _sz, [_i, _i, _i, _i])
-_kv8_write = _sig("dllm_kv8_write", _i, [vp, _i, vp, _i, vp, vp, _i, _i, _i, _i, _i, _i, vp, vp,
+_kv8_write = _sig("dllm_kv8_write", _i, [vp, _n, vp, _n, vp, vp, _n, _n, _n, _n, _n, _n, vp, vp,
                                          vp, vp, vp, _sz, vp])
-_kv8_read = _sig("dllm_kv8_read", _i, [vp, vp, vp, vp, vp, vp, _i, _i, _i, _i, _i, _i, vp, _i,
-                                       vp, _i, vp, _sz, vp])
+_kv8_read = _sig("dllm_kv8_read", _i, [vp, vp, vp, vp, vp, vp, _n, _n, _n, _n, _n, _n, vp, _n,
+                                       vp, _n, vp, _sz, vp])
 _attn_kv8_ws = _sig("dllm_attention_kv8_workspace_size", _sz, [_i, _i, _i, _i, _i, _i])
-_attn_kv8 = _sig("dllm_attention_kv8", _i, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, _i, _i, _i,
-                                            _i, _i, _i, _i, vp, _sz, vp])
+_attn_kv8 = _sig("dllm_attention_kv8", _i, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, _n, _n, _n,
+                                            _n, _n, _n, _n, vp, _sz, vp])
 _gemm_ws = _sig("dllm_gemm_workspace_size", _sz, [_i, _i, _i, _i])
 _gemm = _sig("dllm_gemm_bf16", _i, [vp, vp, vp, _i, _i, _i, _i, _i, vp, _sz, vp])
 _gemm_stall = _sig("dllm_selftest_gemm_stall", _i, [vp, vp, vp, _i, _i, _i, vp, _sz, vp])
