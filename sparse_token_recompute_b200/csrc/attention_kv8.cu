@@ -17,9 +17,12 @@
 // The K scale multiplies the fp32 score.  The V scale 2^e of a key's block is an
 // addend of its exponent: with x_j = score_j + e_j (log2 units) and a reference
 // r at most 8 below the largest x_j,
-//   O = sum_j 2^(x_j - r) v8_j,   l = sum_j 2^(x_j - r) 2^-e_j,   out = O / l,
-// so that the keys with the largest weight * scale have the weights near 1, and
-// f16's range is kept however far apart the blocks' scales are.
+//   O = sum_j 2^(x_j - r) v8_j,   l = sum_j 2^(score_j - r'),   out = O / l * 2^(r - r'),
+// so that the keys with the largest weight * scale have the weights near 1.  The sum
+// has a reference r' of its own, near the largest score, and takes a weight as
+// 2^(x_j - r) * 2^-e_j * 2^(r - r').  Where 2^e_j or 2^(r - r') is far from 1
+// (kKv8Far) the first factor may flush to zero though the weight counts (a block of
+// zero V rows has the scale 2^-100): there the score is exponentiated anew.
 #include <algorithm>
 #include <type_traits>
 
@@ -213,7 +216,9 @@ __global__ void __launch_bounds__(RW * 32, 4)
   float o[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {kKv8NoRef, kKv8NoRef};  // the weights' reference
+  float lm[2] = {kKv8NoRef, kKv8NoRef}, l[2] = {0.f, 0.f};  // the sum and its own
+  float fc[2] = {1.f, 1.f};                                 // and what lies between them
 
   // Column n of an 8-key score tile is key key8(n): at head_dim 128 rows 4 apart in
   // neighbouring lanes, whose swizzled 16-byte pieces lie on different banks; V's 16-byte
@@ -278,14 +283,8 @@ __global__ void __launch_bounds__(RW * 32, 4)
         else
           lds64(w[x], base + v_at[x]);
       }
-      float ev, inv_v;
-      v_scale_parts(sc.y, ev, inv_v);
-      const float k0 = rs[0] * sc.x, k1 = rs[1] * sc.x;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        s[n][0] = fmaf(s[n][0], k0, ev), s[n][1] = fmaf(s[n][1], k0, ev);
-        s[n][2] = fmaf(s[n][2], k1, ev), s[n][3] = fmaf(s[n][3], k1, ev);
-      }
+      const float ev = v_exponent(sc.y), inv_v = v_inverse(sc.y);
+      const float k[2] = {rs[0] * sc.x, rs[1] * sc.x};  // log2 units per raw score
       if (left < RK) {  // what lies past the last key plays no part, whatever it holds
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -298,21 +297,37 @@ __global__ void __launch_bounds__(RW * 32, 4)
           for (int y = 0; y < L::VB / 4; ++y)
             if (v_key[x] >= left) w[x][y] = 0;
       }
-      float alpha[2] = {1.f, 1.f};
-      bool grew = false;
+      float top[2], f[2], alpha[2] = {1.f, 1.f};
+      bool up[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (mx > m[x] + kKv8Lazy) {
-          alpha[x] = exp2_approx(m[x] - mx);
-          m[x] = mx;
-          grew = true;
-        }
+        top[x] = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * k[x];
+        up[x] = top[x] + ev > m[x] + kKv8Lazy;
+        f[x] = fc[x] * inv_v;  // 0: far
       }
-      if (__any_sync(0xffffffffu, grew)) {
-        l[0] *= alpha[0], l[1] *= alpha[1];
+      if (__any_sync(0xffffffffu, up[0] || up[1] || f[0] == 0.f || f[1] == 0.f)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (up[x]) {
+            alpha[x] = exp2_approx(m[x] - (top[x] + ev));
+            m[x] = top[x] + ev;
+          }
+          if (top[x] > lm[x] && (up[x] || f[x] == 0.f)) {
+            l[x] *= exp2_approx(lm[x] - top[x]);
+            lm[x] = top[x];
+          }
+          fc[x] = ref_factor(m[x] - lm[x]);
+          f[x] = fc[x] * inv_v;
+          if (f[x] == 0.f) {  // the weights anew
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int n = y >> 1, i = y & 1;
+              if (8 * n + key8(2 * t + i) < left) l[x] += exp2_approx(fmaf(s[n][2 * x + i], k[x], -lm[x]));
+            }
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           o[n][0] *= alpha[0], o[n][1] *= alpha[0], o[n][2] *= alpha[1], o[n][3] *= alpha[1];
@@ -321,9 +336,17 @@ __global__ void __launch_bounds__(RW * 32, 4)
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) p[n][x] = exp2_approx(s[n][x] - m[x >> 1]);
-      l[0] = fmaf((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]), inv_v, l[0]);
-      l[1] = fmaf((p[0][2] + p[0][3]) + (p[1][2] + p[1][3]), inv_v, l[1]);
+        for (int x = 0; x < 4; ++x) p[n][x] = exp2_approx(fmaf(s[n][x], k[x >> 1], ev - m[x >> 1]));
+      if (left < RK) {  // (-infinity times a zero scale is NaN)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (8 * n + key8(2 * t + (x & 1)) >= left) p[n][x] = 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        l[x] = fmaf((p[0][2 * x] + p[0][2 * x + 1]) + (p[1][2 * x] + p[1][2 * x + 1]), f[x], l[x]);
       const uint32_t pa[4] = {pack_h2(p[0][0], p[0][1]), pack_h2(p[0][2], p[0][3]),
                               pack_h2(p[1][0], p[1][1]), pack_h2(p[1][2], p[1][3])};
 #pragma unroll
@@ -356,10 +379,17 @@ __global__ void __launch_bounds__(RW * 32, 4)
     float sum = l[i];
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    // the warp's output: its sums over its own softmax sum, and the references' difference
+    // in two factors, either of which alone stays a normal float
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum, f = exp2_approx(0.5f * (m[i] - lm[i]));
+    normal_stats(lm[i], sum);
     if (t == 0) {
       float* x = ml + (warp * RM + g + 8 * i) * 2;
-      x[0] = m[i], x[1] = sum;
+      x[0] = lm[i], x[1] = sum;
     }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      o[j][2 * i] = o[j][2 * i] * inv * f * f, o[j][2 * i + 1] = o[j][2 * i + 1] * inv * f * f;
     // n-tile j of lane t: byte j of V's pieces piece8(2t) and piece8(2t + 1)
     float* dst = red + (warp * RM + g + 8 * i) * HD;
 #pragma unroll
@@ -378,22 +408,22 @@ __global__ void __launch_bounds__(RW * 32, 4)
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < RW; ++w) mx = fmaxf(mx, ml[(w * RM + row) * 2]);
-    float sum = 0.f, acc[8];
+    float sum = 0.f, part[RW], acc[8];
+#pragma unroll
+    for (int w = 0; w < RW; ++w) {
+      const float* x = ml + (w * RM + row) * 2;
+      part[w] = x[1] == 0.f ? 0.f : x[1] * exp2_approx(x[0] - mx);  // (0: no keys)
+      sum += part[w];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // a row without keys: zeros
 #pragma unroll
     for (int x = 0; x < 8; ++x) acc[x] = 0.f;
 #pragma unroll
     for (int w = 0; w < RW; ++w) {
-      const float* x = ml + (w * RM + row) * 2;
-      if (x[1] == 0.f) continue;  // no keys
-      const float f = exp2_approx(x[0] - mx);
-      sum += x[1] * f;
       const float* src = red + (w * RM + row) * HD + e;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = fmaf(src[k], f, acc[k]);
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(src[k], part[w] * inv, acc[k]);
     }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // a row without keys: zeros
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= inv;
     const int r = tile * RM + row;
     const size_t at = (size_t)(off + r / A.G) * A.Hq + kvh * A.G + r % A.G;
     if (A.S == 1) {

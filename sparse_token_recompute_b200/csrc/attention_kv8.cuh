@@ -9,6 +9,12 @@ namespace dllm {
 
 constexpr float kKv8Log2e = 1.4426950408889634f;
 constexpr float kKv8Lazy = 8.0f;  // how far below the largest x_j the reference may stay
+// V scales and references whose exponents (their differences) are larger than this are far:
+// the weights' way into the sum, p_j 2^-e_j 2^(r - r'), could leave the range of floats
+constexpr int kKv8Far = 30;
+// what a reference starts with: below any score, and finite, so that a score of -infinity
+// has the weight 0 from the start
+constexpr float kKv8NoRef = -3.0e38f;
 
 constexpr int kKv8MaxShares = 64;
 
@@ -47,13 +53,17 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 __device__ __forceinline__ float pow2i(int e) {
   return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23);
 }
-// log2 and inverse of a block's V scale; a block that holds no rows (its codes are zeros)
-// counts as scale 1
-__device__ __forceinline__ void v_scale_parts(float s, float& log2s, float& inv) {
-  const bool holds = s >= kKv8MinScale;
-  log2s = holds ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
-  inv = holds ? kv8_inverse(s) : 1.f;
+// log2 of a block's V scale; -infinity for a block that holds no rows (its values are zeros)
+__device__ __forceinline__ float v_exponent(float s) {
+  return s >= kKv8MinScale ? (float)((int)(__float_as_uint(s) >> 23) - 127) : -INFINITY;
 }
+// its inverse, 0 if it is far from 1
+__device__ __forceinline__ float v_inverse(float s) {
+  constexpr float lo = 1.0f / (1 << kKv8Far), hi = 1 << kKv8Far;
+  return s >= lo && s <= hi ? kv8_inverse(s) : 0.f;
+}
+// 2^(weights' reference - sum's reference), 0 if that is far above 1
+__device__ __forceinline__ float ref_factor(float d) { return d <= (float)kKv8Far ? exp2_approx(d) : 0.f; }
 // (m, l) with the same l 2^m and 1 <= l < 2; l = 0 stays, with m = -inf
 __device__ __forceinline__ void normal_stats(float& m, float& l) {
   if (l == 0.f) m = -INFINITY;

@@ -216,10 +216,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
     for (int j = 0; j < T; ++j) {
       fetch(j + 1);
       if (!is_v && warp == (j & 1)) {
+        // (the sum takes the whole tile one way: a far scale makes it far)
+        const bool near = __all_sync(0xffffffffu, lane >= 4 || key0 + j * BK + lane * 16 >= len || v_inverse(sc.y) != 0.f);
         if (lane < 4) {
-          float4 f = make_float4(sc.x, 0.f, 0.f, 0.f);
-          if (key0 + j * BK + lane * 16 < len) v_scale_parts(sc.y, f.y, f.z);
-          scales[j % NSC * 4 + lane] = f;
+          scales[j % NSC * 4 + lane] = make_float4(sc.x, v_exponent(sc.y), near ? v_inverse(sc.y) : 0.f, 0.f);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sc_full(j));
@@ -333,8 +333,40 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full);
     }
-    float m = -INFINITY, l = 0.f;
+    float m = kKv8NoRef;            // the weights' reference
+    float lm = kKv8NoRef, l = 0.f;  // the sum and its own
+    float fc = 1.f;                 // and what lies between them
     bool ok = true;
+    // the sum's reference moves up to r
+    auto raise_sum = [&](float r) {
+      if (r > lm) {
+        l *= exp2_approx(lm - r);
+        lm = r;
+      }
+      fc = ref_factor(m - lm);
+    };
+    // Adds the weights of tile j to the sum where its scales or references are far, from the
+    // scores anew.  (Seldom: not unrolled.)
+    auto far_sum = [&](bool far, const float4* sc, int j, int nkeys) {
+      float top = kKv8NoRef;
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {
+#pragma unroll 1
+        for (int g = 0; g < 4 && 16 * g < nkeys; ++g) {
+          float t[16];
+          __syncwarp();
+          tmem_ld16(tS(j) + lane_off + 16 * g, t);
+          const float k = rs * sc[g].x;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (16 * g + i >= nkeys) continue;
+            if (turn == 0) top = fmaxf(top, t[i] * k);
+            else if (far) l += exp2_approx(fmaf(t[i], k, -lm));
+          }
+        }
+        if (turn == 0 && far) raise_sum(top);
+      }
+    };
     // a warp whose 32 rows are all past the sequence's rows takes no further part
     if (quad < live_warps) {
       for (int j = 0; j < T; ++j) {
@@ -342,11 +374,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
                                          mbar_wait(s_full(j), par(j), abort_flag, status));
         if (!ok) break;
         tc_fence_after();
+        const float4* sc = scales + j % NSC * 4;
+        const int nkeys = len - (k_lo + j) * BK;
+        const bool far = fc == 0.f || sc[0].z == 0.f;
+        if (__any_sync(0xffffffffu, far)) far_sum(far, sc, j, nkeys);
         float s[BK];
         tmem_ld32_nowait(tS(j) + lane_off, s);
         tmem_ld32_nowait(tS(j) + lane_off + 32, s + 32);
-        const float4* sc = scales + j % NSC * 4;
-        const int nkeys = len - (k_lo + j) * BK;
         tmem_wait_ld();
         auto tile_softmax = [&](auto last) {
           constexpr bool LAST = decltype(last)::value;  // some of the keys do not exist
@@ -371,8 +405,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
           const bool need = mx > m + kKv8Lazy;
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = need ? exp2_approx(m - mx) : 1.f;  // the first time: 0
-            if (need) m = mx;
-            l *= alpha;
+            if (need) {
+              m = mx;
+              raise_sum(sc[0].z != 0.f ? m - sc[0].y : lm);
+            }
             if (j > 0) {
               // O may be rescaled once PV(j-1) is complete, until P(j) is handed over
               if (!__all_sync(0xffffffffu, mbar_wait(pv_done(j - 1), par(j - 1), abort_flag, status)))
@@ -388,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
               }
             }
           }
+          float add = 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t pk[16];
@@ -410,11 +447,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
                 sum = add_f32x2(sum, p);
                 pk[c / 2 - 16 * h] = pack_h2(p.x, p.y);
               }
-              l = fmaf(sum.x + sum.y, f.z, l);
+              add = fmaf(sum.x + sum.y, f.z, add);
             }
             // P over scores that have been read
             tmem_st16(tS(j) + lane_off + 16 * h, pk);
           }
+          l = fmaf(add, far ? 0.f : fc, l);
           return true;
         };
         ok = nkeys < BK ? tile_softmax(std::true_type{}) : tile_softmax(std::false_type{});
@@ -428,6 +466,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       tc_fence_after();
       if (ok) {
         const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row without keys: zeros
+        // the references' difference, in two factors that stay normal floats
+        const float ref = exp2_approx(0.5f * (m - lm));
         const size_t pa = (size_t)share * A.part_rows * A.Hq + at;
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
@@ -440,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
           }
           if (!there) continue;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
+          for (int i = 0; i < 32; ++i) o[i] = o[i] * inv * ref * ref;
           if (A.S > 1) {
             if (T > 0) {
 #pragma unroll
@@ -454,12 +494,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
           }
         }
         if (there && (A.S > 1 || A.st_m)) {
-          normal_stats(m, l);
+          normal_stats(lm, l);
           if (A.S > 1) {
-            A.part_ml[pa * 2] = m;
+            A.part_ml[pa * 2] = lm;
             A.part_ml[pa * 2 + 1] = l;
           } else {
-            A.st_m[at] = m / kKv8Log2e;
+            A.st_m[at] = lm / kKv8Log2e;
             A.st_l[at] = l;
           }
         }
