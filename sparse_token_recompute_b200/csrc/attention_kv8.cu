@@ -15,11 +15,19 @@
 //           of the largest stay normal numbers;
 //   P       exp2(score - reference), rounded to f16's 11 bits (bf16 would keep 8).
 // The K scale multiplies the fp32 score.  The V scale 2^e of a key's block is an
-// addend of its exponent: with x_j = score_j + e_j (log2 units) and a reference
-// r at most 8 below the largest x_j,
-//   O = sum_j 2^(x_j - r) v8_j,   l = sum_j 2^(score_j - r'),   out = O / l * 2^(r - r'),
-// so that the keys with the largest weight * scale have the weights near 1.  The sum
-// has a reference r' of its own, near the largest score, and takes a weight as
+// addend of its exponent: with x_j = score_j + e_j (log2 units) and a reference r,
+//   O = sum_j 2^(x_j - r) v8_j,   l = sum_j 2^(score_j - r'),   out = O / l * 2^(r - r').
+//
+// f16 keeps 11 bits of a weight down to 2^-14 and has none below 2^-25, and a tile of keys
+// may matter although another one's weights are far larger: that one's codes may be small
+// (a scale left behind by an outlier) or zero in a channel.  So r follows the keys, up and
+// down, such that each tile's largest weight is 2^-4 .. 2^15 in f16; O, in fp32, is rescaled
+// where r moves.  A weight is then off by at most 2^-11 of itself, or 2^-21 of the largest
+// weight * scale of its own tile: 16 keys here, 64 of the tcgen05 kernel, which also brings
+// the codes of a tile of several blocks towards one scale.  r falls by 2^64 at most; tiles
+// below that lose bits from 2^-84 of the largest weight * scale on.
+//
+// The sum has a reference r' of its own, near the largest score, and takes a weight as
 // 2^(x_j - r) * 2^-e_j * 2^(r - r').  Where 2^e_j or 2^(r - r') is far from 1
 // (kKv8Far) the first factor may flush to zero though the weight counts (a block of
 // zero V rows has the scale 2^-100): there the score is exponentiated anew.
@@ -216,9 +224,9 @@ __global__ void __launch_bounds__(RW * 32, 4)
   float o[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m[2] = {kKv8NoRef, kKv8NoRef};  // the weights' reference
-  float lm[2] = {kKv8NoRef, kKv8NoRef}, l[2] = {0.f, 0.f};  // the sum and its own
-  float fc[2] = {1.f, 1.f};                                 // and what lies between them
+  float m[2] = {kKv8NoRef, kKv8NoRef}, low[2] = {-INFINITY, -INFINITY};  // the weights' reference
+  float lm[2] = {kKv8NoRef, kKv8NoRef}, l[2] = {0.f, 0.f};               // the sum and its own
+  float fc[2] = {1.f, 1.f};                                              // and what lies between them
 
   // Column n of an 8-key score tile is key key8(n): at head_dim 128 rows 4 apart in
   // neighbouring lanes, whose swizzled 16-byte pieces lie on different banks; V's 16-byte
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(RW * 32, 4)
         else
           lds64(w[x], base + v_at[x]);
       }
-      const float ev = v_exponent(sc.y), inv_v = v_inverse(sc.y);
+      const float ev = v_exponent(sc.y), inv_v = near_inverse(sc.y);
       const float k[2] = {rs[0] * sc.x, rs[1] * sc.x};  // log2 units per raw score
       if (left < RK) {  // what lies past the last key plays no part, whatever it holds
 #pragma unroll
@@ -298,23 +306,23 @@ __global__ void __launch_bounds__(RW * 32, 4)
             if (v_key[x] >= left) w[x][y] = 0;
       }
       float top[2], f[2], alpha[2] = {1.f, 1.f};
-      bool up[2];
+      bool move[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        top[x] = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * k[x];
-        up[x] = top[x] + ev > m[x] + kKv8Lazy;
+        top[x] = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        move[x] = wants_ref(fmaf(top[x], k[x], ev - m[x]));
         f[x] = fc[x] * inv_v;  // 0: far
       }
-      if (__any_sync(0xffffffffu, up[0] || up[1] || f[0] == 0.f || f[1] == 0.f)) {
+      if (__any_sync(0xffffffffu, move[0] || move[1] || f[0] == 0.f || f[1] == 0.f)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (up[x]) {
-            alpha[x] = exp2_approx(m[x] - (top[x] + ev));
-            m[x] = top[x] + ev;
-          }
-          if (top[x] > lm[x] && (up[x] || f[x] == 0.f)) {
+          top[x] *= k[x];
+          const float before = m[x];
+          move[x] = new_ref(top[x] + ev, m[x], low[x]);
+          if (move[x]) alpha[x] = exp2_approx(before - m[x]);
+          if (top[x] > lm[x] && (move[x] || f[x] == 0.f)) {
             l[x] *= exp2_approx(lm[x] - top[x]);
             lm[x] = top[x];
           }

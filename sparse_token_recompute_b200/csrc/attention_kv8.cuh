@@ -8,7 +8,13 @@
 namespace dllm {
 
 constexpr float kKv8Log2e = 1.4426950408889634f;
-constexpr float kKv8Lazy = 8.0f;  // how far below the largest x_j the reference may stay
+// Where the largest weight of a tile lies in f16: a reference puts it at 2^6, and stays while
+// it is 2^-4 .. 2^15 (a move makes O wait and be rescaled: over random scales of four octaves
+// 0.6 moves per warp and 24 tiles; 3.3, and 4 % of the time, for 2^0 .. 2^15 around 2^8).
+// References fall at most 2^64 below the highest one so far, so that sums which grow with
+// every fall stay floats; a tile is left where it is if even there its weights were below
+// 2^-24.
+constexpr float kKv8Aim = 6.0f, kKv8Low = -4.0f, kKv8High = 15.0f, kKv8Fall = 64.0f, kKv8Lost = 24.0f;
 // V scales and references whose exponents (their differences) are larger than this are far:
 // the weights' way into the sum, p_j 2^-e_j 2^(r - r'), could leave the range of floats
 constexpr int kKv8Far = 30;
@@ -57,10 +63,21 @@ __device__ __forceinline__ float pow2i(int e) {
 __device__ __forceinline__ float v_exponent(float s) {
   return s >= kKv8MinScale ? (float)((int)(__float_as_uint(s) >> 23) - 127) : -INFINITY;
 }
-// its inverse, 0 if it is far from 1
-__device__ __forceinline__ float v_inverse(float s) {
+// the inverse of a power of two, 0 if it is far from 1
+__device__ __forceinline__ float near_inverse(float s) {
   constexpr float lo = 1.0f / (1 << kKv8Far), hi = 1 << kKv8Far;
   return s >= lo && s <= hi ? kv8_inverse(s) : 0.f;
+}
+// whether a tile whose largest x_j lies d above the reference wants another one
+__device__ __forceinline__ bool wants_ref(float d) {
+  return fabsf(d - 0.5f * (kKv8High + kKv8Low)) > 0.5f * (kKv8High - kKv8Low);
+}
+// moves the reference m to the tile's largest x_j, mx, but not below `low`; false: it stays
+__device__ __forceinline__ bool new_ref(float mx, float& m, float& low) {
+  if (!wants_ref(mx - m) || !(mx > low - kKv8Lost) || (mx < m && m <= low)) return false;
+  m = fmaxf(mx - kKv8Aim, low);
+  low = fmaxf(low, m - kKv8Fall);
+  return true;
 }
 // 2^(weights' reference - sum's reference), 0 if that is far above 1
 __device__ __forceinline__ float ref_factor(float d) { return d <= (float)kKv8Far ? exp2_approx(d) : 0.f; }

@@ -68,7 +68,8 @@ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-template <int HD>
+// MIX: blocks shorter than a tile of keys, whose V scales may differ within it
+template <int HD, bool MIX>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args A) {
   using L = Smem<HD>;
   griddep_launch_dependents();
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   if (warp < NC) {
     fetch(0);
     if (!is_v) sc = fetch_scales(warp);
+    else if (MIX) sc = fetch_scales(0);
   }
   // and a softmax thread's query row
   const int r = (warp & 3) * 32 + lane;  // packed row in the tile (= TMEM lane)
@@ -213,14 +215,34 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
 
   if (warp < NC) {
     // ---------------------------------------------------------------- converters
+    // Blocks shorter than a tile: where the V scales of a tile span more than six octaves, the
+    // codes themselves are brought towards a common scale, as far as f16 holds them exactly
+    // (their last bit is 2^-9, the largest 448: by 2^-15 .. 2^7), so that the weights' range
+    // is not spent on it.  Exponent of the factor for the group of 16 keys of lane 0 .. 3.
+    auto v_shift = [&](float e) {
+      float hi = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+      float lo = e == -INFINITY ? INFINITY : e;
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
+      return hi - lo > 6.f ? fminf(fmaxf(e - hi + 7.f, -15.f), 7.f) : 0.f;
+    };
     for (int j = 0; j < T; ++j) {
       fetch(j + 1);
+      // of this warp's two groups of a V tile
+      float shift[2] = {0.f, 0.f};
+      if (MIX && is_v) {
+        const float c = v_shift(v_exponent(sc.y));
+        shift[0] = __shfl_sync(0xffffffffu, c, (warp & 1) * 2);
+        shift[1] = __shfl_sync(0xffffffffu, c, (warp & 1) * 2 + 1);
+        sc = fetch_scales(j + 1);
+      }
       if (!is_v && warp == (j & 1)) {
+        const float e = v_exponent(sc.y), c = MIX ? v_shift(e) : 0.f;
         // (the sum takes the whole tile one way: a far scale makes it far)
-        const bool near = __all_sync(0xffffffffu, lane >= 4 || key0 + j * BK + lane * 16 >= len || v_inverse(sc.y) != 0.f);
-        if (lane < 4) {
-          scales[j % NSC * 4 + lane] = make_float4(sc.x, v_exponent(sc.y), near ? v_inverse(sc.y) : 0.f, 0.f);
-        }
+        const float inv = near_inverse(sc.y) * (MIX ? pow2i((int)c) : 1.f);
+        const bool near = __all_sync(0xffffffffu, lane >= 4 || key0 + j * BK + lane * 16 >= len || inv != 0.f);
+        if (lane < 4) scales[j % NSC * 4 + lane] = make_float4(sc.x, e - c, near ? inv : 0.f, 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(sc_full(j));
         sc = fetch_scales(j + 2);
@@ -232,19 +254,33 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       if (!mbar_wait(empty_at(bar), (turn & 1) ^ 1, abort_flag, status)) break;
       const uint32_t dst = st0 + slot * L::SLOT;
       const uint32_t from = raw + (j & 1) * L::RAW;
+      auto convert = [&](auto shifted) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        uint32_t q[4], h[8];
-        lds128(q, from + i * 1024);
+        for (int i = 0; i < NV; ++i) {
+          uint32_t q[4], h[8];
+          lds128(q, from + i * 1024);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e4m3x4_to_f16x4(q[k], h[2 * k], h[2 * k + 1]);
-        const uint32_t to = dst + i % HB * (BK * 128) + i / HB * 1024;
+          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x4(q[k], h[2 * k], h[2 * k + 1]);
+          if constexpr (decltype(shifted)::value) {
+            const __half2 f = __float2half2_rn(pow2i((int)shift[i / HB / 2]));
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(c ? to ^ 16 : to), "r"(h[4 * c]),
-                       "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
-                       : "memory");
-      }
+            for (int k = 0; k < 8; ++k) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), f);
+              h[k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+          const uint32_t to = dst + i % HB * (BK * 128) + i / HB * 1024;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(c ? to ^ 16 : to), "r"(h[4 * c]),
+                         "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
+                         : "memory");
+        }
+      };
+      if (MIX && (shift[0] != 0.f || shift[1] != 0.f))
+        convert(std::true_type{});
+      else
+        convert(std::false_type{});
       // generic stores before the tensor core's reads
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -333,9 +369,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(q_full);
     }
-    float m = kKv8NoRef;            // the weights' reference
-    float lm = kKv8NoRef, l = 0.f;  // the sum and its own
-    float fc = 1.f;                 // and what lies between them
+    float m = kKv8NoRef, low = -INFINITY;  // the weights' reference
+    float lm = kKv8NoRef, l = 0.f;         // the sum and its own
+    float fc = 1.f;                        // and what lies between them
     bool ok = true;
     // the sum's reference moves up to r
     auto raise_sum = [&](float r) {
@@ -402,14 +438,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
             const float2 f = *reinterpret_cast<const float2*>(sc + g);
             if (!LAST || 16 * g < nkeys) mx = fmaxf(mx, fmaf(fmaxf(a, c), rs * f.x, f.y));
           }
-          const bool need = mx > m + kKv8Lazy;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? exp2_approx(m - mx) : 1.f;  // the first time: 0
-            if (need) {
-              m = mx;
-              raise_sum(sc[0].z != 0.f ? m - sc[0].y : lm);
-            }
-            if (j > 0) {
+          if (__any_sync(0xffffffffu, wants_ref(mx - m))) {
+            const float before = m;
+            const bool move = new_ref(mx, m, low);
+            const float alpha = move ? exp2_approx(before - m) : 1.f;  // the first time: 0
+            if (move) raise_sum(sc[0].z != 0.f ? m - sc[0].y : lm);
+            if (j > 0 && __any_sync(0xffffffffu, move)) {
               // O may be rescaled once PV(j-1) is complete, until P(j) is handed over
               if (!__all_sync(0xffffffffu, mbar_wait(pv_done(j - 1), par(j - 1), abort_flag, status)))
                 return false;
@@ -518,8 +552,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
 }  // namespace
 
 cudaError_t launch_attention_kv8_tc(const Kv8Args& A, long long ctas, int hd, cudaStream_t s) {
-  return hd == 128 ? launch_kv8<attn_kv8_tc_kernel<128>>((unsigned)ctas, kThreads, Smem<128>::TOTAL, s, A)
-                   : launch_kv8<attn_kv8_tc_kernel<64>>((unsigned)ctas, kThreads, Smem<64>::TOTAL, s, A);
+  auto go = [&](auto hd_c, auto mix) {
+    constexpr int HD = decltype(hd_c)::value;
+    return launch_kv8<attn_kv8_tc_kernel<HD, decltype(mix)::value>>((unsigned)ctas, kThreads, Smem<HD>::TOTAL, s, A);
+  };
+  auto of_hd = [&](auto mix) {
+    return hd == 128 ? go(std::integral_constant<int, 128>{}, mix) : go(std::integral_constant<int, 64>{}, mix);
+  };
+  return (1 << A.blk_log2) < BK ? of_hd(std::true_type{}) : of_hd(std::false_type{});
 }
 
 }  // namespace dllm

@@ -1,9 +1,13 @@
 """Attention over 8-bit caches whose V scales lie far apart: the softmax sum, which no
 V scale may touch, and the weights, which f16 holds, against the oracle in 64 bits."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv8 import BF, check_attention, filled, normal
+from _util import f64
+from test_gpu_kv8 import BF, check_attention, decoded, filled, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +48,115 @@ def test_only_blocks_of_zeros(lib, rows):
         got.append(st)
     lse = [m + torch.log(l) for _, m, l in got]
     assert torch.all(got[1][0] == 0) and torch.allclose(lse[0], lse[1], rtol=2.0 ** -20, atol=2.0 ** -20)
+
+
+# ------------------------------------------------------------------ weights
+
+def weight_bound(q, K, V, vs):
+    """One head: the output [R, hd] of q [R, hd] over K, V [n, hd] (vs [n]: V's scales) and a bound
+    of its error before the store.  Weights come in tiles of 64 keys (16 where few rows ask).  With
+    the largest weight * scale of a tile brought to 2^-4 or more, f16 holds the others to half a
+    step, 2^-11 of each, or to 2^-25 where they are below 2^-14: 2^-21 of the largest.  Where a tile's scales span more than six
+    octaves its codes are first brought towards a common scale, by 2^-15 .. 2^7."""
+    n, hd = K.shape
+    s = q @ K.T / math.sqrt(hd)
+    p = np.exp(s - s.max(1, keepdims=True))
+    l = p.sum(1, keepdims=True)
+    mag = np.abs(q) @ np.abs(K).T / math.sqrt(hd)
+    ds = ((hd / 16 + 2) * 2.0 ** -23 * mag + 2.0 ** -22 * np.abs(s)).max(1, keepdims=True)
+    tol = (2.0 ** -11 + 2 * ds + n / 16 * 2.0 ** -23 + 2.0 ** -20) * (p @ np.abs(V))
+    for t in range(0, n, 64):
+        e = np.log2(vs[t:t + 64])
+        c = np.clip(e - e.max() + 7, -15, 7) if e.max() - e.min() > 6 else 0.0
+        unit = 2.0 ** (e - c)
+        tol += 2.0 ** -21 * (p[:, t:t + 64] * unit).max(1, keepdims=True) * (np.abs(V[t:t + 64]) / unit[:, None]).sum(0)
+    return p @ V / l, tol / l, p @ np.abs(V) / l
+
+
+def check_weights(lib, q, cache, block, rows, where):
+    """Against the bound, which must itself be within 2^-10 of what the output is made of."""
+    k8, ks, v8, vs = cache
+    B, N, H, hd = k8.shape
+    o = torch.full_like(q, 7.0)
+    cnt = torch.full((B,), rows, dtype=torch.int32, device="cuda")
+    ws = lib.dllm_attention_kv8(q, k8, ks, v8, vs, o, cnt, rows, block)
+    assert ws.device_status() == 0
+    for b, h in where:
+        one = lambda c, sc: decoded(c[b:b + 1, :, h:h + 1], sc[b:b + 1, h:h + 1], block)[0, :, 0]
+        at = lambda t: f64(t.view(B, rows, H, hd)[b, :, h])
+        ref, tol, size = weight_bound(at(q), one(k8, ks), one(v8, vs), f64(vs[b, h]).repeat(block)[:N])
+        assert np.all(tol <= 2.0 ** -10 * size)
+        err = np.abs(at(o) - ref) - (tol + 2.0 ** -8 * (np.abs(ref) + tol))
+        assert np.all(err <= 0), (b, h, err.max())
+
+
+UNITS = (74, 8)   # sequences and heads for which one CTA passes over all keys
+
+
+def many(cache):
+    """The cache of one sequence and head, as UNITS equal ones."""
+    B, H = UNITS
+    k8, ks, v8, vs = (t.view(torch.uint8) if i % 2 == 0 else t for i, t in enumerate(cache))
+    code = lambda t: t.expand(B, -1, H, -1).contiguous().view(torch.float8_e4m3fn)
+    scale = lambda t: t.expand(B, H, -1).contiguous()
+    return code(k8), scale(ks), code(v8), scale(vs)
+
+
+WHERE = [(0, 0), (UNITS[0] - 1, UNITS[1] - 1)]
+
+
+@pytest.mark.parametrize("rows", [1, 130])
+@pytest.mark.parametrize("block", [16, 64, 128])
+@pytest.mark.parametrize("far", [9, 24, 30])
+def test_a_scale_left_behind_by_an_outlier(lib, rows, block, far):
+    """A row 2^far times larger than the others raises its block's scale and is then written anew
+    at their size: the scale stays, the block's codes become small or zero."""
+    N, hd = 1024, 128
+    cache = lib.kv8_cache(1, N, 1, hd, block)
+    k, v = normal((N, hd), 1).to(BF), (normal((N, hd), 2) + 0.3).to(BF)
+    lib.dllm_kv8_write(k, v, None, None, *cache, block)
+    idx = torch.tensor([[333]], dtype=torch.int32, device="cuda")
+    row = v[333:334].clone()
+    for x in (row * 2.0 ** far, row):
+        lib.dllm_kv8_write(k[333:334], x, idx, None, *cache, block)
+    vs = cache[3][0, 0]
+    assert vs[333 // block] >= 2.0 ** (far - 1) * vs.min()
+    q = normal((UNITS[0] * rows, UNITS[1] * hd), 3) * 0.1
+    check_weights(lib, q.to(BF), many(cache), block, rows, WHERE)
+
+
+@pytest.mark.parametrize("rows", [1, 130])
+@pytest.mark.parametrize("block", [16, 64])
+def test_a_heavy_key_with_one_large_channel(lib, rows, block):
+    """The first of 16384 keys holds most of the weight, and one channel of its V row is 2000:
+    the other keys' part in the other channels stays."""
+    N, hd = 16384, 128
+    cache = lib.kv8_cache(1, N, 1, hd, block)
+    k, v = normal((N, hd), 1), normal((N, hd), 2) + 0.3
+    v[0, 5] = 2000
+    lib.dllm_kv8_write(k.to(BF), v.to(BF), None, None, *cache, block)
+    k0 = k[0] / k[0].norm()
+    q = normal((UNITS[0] * rows, UNITS[1] * hd), 3) * 0.05
+    q += (k0 * 12 * math.sqrt(hd) / k[0].norm()).repeat(UNITS[1])
+    check_weights(lib, q.to(BF), many(cache), block, rows, WHERE)
+
+
+@pytest.mark.parametrize("rows", [1, 130])
+@pytest.mark.parametrize("octaves,blocks", [(1, 78), (3, 25)])
+@pytest.mark.parametrize("rising", [False, True])
+def test_every_block_has_a_channel_of_its_own(lib, rows, octaves, blocks, rising):
+    """V scales that fall (rise) from block to block, each block alone in its channel: every channel
+    is as good as any other, whatever its size beside theirs."""
+    hd, block = 128, 16
+    N = blocks * block
+    k8, ks, v8, vs = lib.kv8_cache(1, N, 1, hd, block)
+    k8.copy_((normal((1, N, 1, hd), 1) * 100).clamp(-448, 448).to(torch.float8_e4m3fn))
+    ks.fill_(2.0 ** -7)
+    code = torch.zeros(1, N, 1, hd, device="cuda")
+    for i in range(blocks):
+        code[0, i * block:(i + 1) * block, 0, i] = 100 * normal((block,), 5 + i)
+    v8.copy_(code.clamp(-448, 448).to(torch.float8_e4m3fn))
+    e = octaves * torch.arange(blocks, device="cuda").float()
+    vs.copy_(torch.exp2(e - e.max() if rising else -e).expand_as(vs))
+    q = normal((UNITS[0] * rows, UNITS[1] * hd), 3) * 0.1
+    check_weights(lib, q.to(BF), many((k8, ks, v8, vs)), block, rows, WHERE)
