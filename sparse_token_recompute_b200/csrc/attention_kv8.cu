@@ -21,11 +21,11 @@
 // f16 keeps 11 bits of a weight down to 2^-14 and has none below 2^-25, and a tile of keys
 // may matter although another one's weights are far larger: that one's codes may be small
 // (a scale left behind by an outlier) or zero in a channel.  So r follows the keys, up and
-// down, such that each tile's largest weight is 2^-4 .. 2^15 in f16; O, in fp32, is rescaled
-// where r moves.  A weight is then off by at most 2^-11 of itself, or 2^-21 of the largest
+// down, such that each tile's largest weight is 2^-6 .. 2^15 in f16; O, in fp32, is rescaled
+// where r moves.  A weight is then off by at most 2^-11 of itself, or 2^-19 of the largest
 // weight * scale of its own tile: 16 keys here, 64 of the tcgen05 kernel, which also brings
 // the codes of a tile of several blocks towards one scale.  r falls by 2^64 at most; tiles
-// below that lose bits from 2^-84 of the largest weight * scale on.
+// below that lose bits from 2^-83 of the largest weight * scale on.
 //
 // The sum has a reference r' of its own, near the largest score, and takes a weight as
 // 2^(x_j - r) * 2^-e_j * 2^(r - r').  Where 2^e_j or 2^(r - r') is far from 1

@@ -8,13 +8,13 @@
 namespace dllm {
 
 constexpr float kKv8Log2e = 1.4426950408889634f;
-// Where the largest weight of a tile lies in f16: a reference puts it at 2^6, and stays while
-// it is 2^-4 .. 2^15 (a move makes O wait and be rescaled: over random scales of four octaves
-// 0.6 moves per warp and 24 tiles; 3.3, and 4 % of the time, for 2^0 .. 2^15 around 2^8).
+// Where the largest weight of a tile lies in f16: a reference puts it at 2^5, and stays while
+// it is 2^-6 .. 2^15 (a move makes O wait and be rescaled: over random scales of four octaves
+// 0.3 moves per warp and 24 tiles; 3.3, and 4 % of the time, for 2^0 .. 2^15 around 2^8).
 // References fall at most 2^64 below the highest one so far, so that sums which grow with
 // every fall stay floats; a tile is left where it is if even there its weights were below
 // 2^-24.
-constexpr float kKv8Aim = 6.0f, kKv8Low = -4.0f, kKv8High = 15.0f, kKv8Fall = 64.0f, kKv8Lost = 24.0f;
+constexpr float kKv8Aim = 5.0f, kKv8Low = -6.0f, kKv8High = 15.0f, kKv8Fall = 64.0f, kKv8Lost = 24.0f;
 // V scales and references whose exponents (their differences) are larger than this are far:
 // the weights' way into the sum, p_j 2^-e_j 2^(r - r'), could leave the range of floats
 constexpr int kKv8Far = 30;

@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   if (warp < NC) {
     fetch(0);
     if (!is_v) sc = fetch_scales(warp);
-    else if (MIX) sc = fetch_scales(0);
   }
   // and a softmax thread's query row
   const int r = (warp & 3) * 32 + lane;  // packed row in the tile (= TMEM lane)
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
     // Blocks shorter than a tile: where the V scales of a tile span more than six octaves, the
     // codes themselves are brought towards a common scale, as far as f16 holds them exactly
     // (their last bit is 2^-9, the largest 448: by 2^-15 .. 2^7), so that the weights' range
-    // is not spent on it.  Exponent of the factor for the group of 16 keys of lane 0 .. 3.
+    // is not spent on it.  Exponent of the factor of lane's (0 .. 3) group of 16 keys.
     auto v_shift = [&](float e) {
       float hi = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
@@ -227,42 +226,41 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
       return hi - lo > 6.f ? fminf(fmaxf(e - hi + 7.f, -15.f), 7.f) : 0.f;
     };
-    for (int j = 0; j < T; ++j) {
-      fetch(j + 1);
-      // of this warp's two groups of a V tile
-      float shift[2] = {0.f, 0.f};
-      if (MIX && is_v) {
-        const float c = v_shift(v_exponent(sc.y));
-        shift[0] = __shfl_sync(0xffffffffu, c, (warp & 1) * 2);
-        shift[1] = __shfl_sync(0xffffffffu, c, (warp & 1) * 2 + 1);
-        sc = fetch_scales(j + 1);
-      }
-      if (!is_v && warp == (j & 1)) {
-        const float e = v_exponent(sc.y), c = MIX ? v_shift(e) : 0.f;
-        // (the sum takes the whole tile one way: a far scale makes it far)
-        const float inv = near_inverse(sc.y) * (MIX ? pow2i((int)c) : 1.f);
-        const bool near = __all_sync(0xffffffffu, lane >= 4 || key0 + j * BK + lane * 16 >= len || inv != 0.f);
-        if (lane < 4) scales[j % NSC * 4 + lane] = make_float4(sc.x, e - c, near ? inv : 0.f, 0.f);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sc_full(j));
-        sc = fetch_scales(j + 2);
-      }
-      cp_wait<1>();
-      const int slot = is_v ? j % L::VS : j % L::KS;
-      const int turn = is_v ? j / L::VS : j / L::KS;
-      const int bar = is_v ? L::KS + slot : slot;
-      if (!mbar_wait(empty_at(bar), (turn & 1) ^ 1, abort_flag, status)) break;
-      const uint32_t dst = st0 + slot * L::SLOT;
-      const uint32_t from = raw + (j & 1) * L::RAW;
-      auto convert = [&](auto shifted) {
+    auto tiles = [&](auto scaled) {
+      constexpr bool SCALED = decltype(scaled)::value;
+      for (int j = 0; j < T; ++j) {
+        fetch(j + 1);
+        float by[2];  // the factors of this warp's two groups
+        if constexpr (SCALED) {
+          if (!mbar_wait(sc_full(j), (j / NSC) & 1, abort_flag, status)) return;
+          by[0] = scales[j % NSC * 4 + (warp & 1) * 2].w;
+          by[1] = scales[j % NSC * 4 + (warp & 1) * 2 + 1].w;
+        } else if (!is_v && warp == (j & 1)) {
+          const float e = v_exponent(sc.y), c = MIX ? v_shift(e) : 0.f;
+          const float inv = near_inverse(sc.y) * (MIX ? pow2i((int)c) : 1.f);
+          // (the sum takes the whole tile one way: a far scale makes it far)
+          const bool near = __all_sync(0xffffffffu, lane >= 4 || key0 + j * BK + lane * 16 >= len || inv != 0.f);
+          if (lane < 4)
+            scales[j % NSC * 4 + lane] = make_float4(sc.x, e - c, near ? inv : 0.f, MIX ? pow2i((int)c) : 1.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sc_full(j));
+          sc = fetch_scales(j + 2);
+        }
+        cp_wait<1>();
+        const int slot = is_v ? j % L::VS : j % L::KS;
+        const int turn = is_v ? j / L::VS : j / L::KS;
+        const int bar = is_v ? L::KS + slot : slot;
+        if (!mbar_wait(empty_at(bar), (turn & 1) ^ 1, abort_flag, status)) return;
+        const uint32_t dst = st0 + slot * L::SLOT;
+        const uint32_t from = raw + (j & 1) * L::RAW;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           uint32_t q[4], h[8];
           lds128(q, from + i * 1024);
 #pragma unroll
           for (int k = 0; k < 4; ++k) e4m3x4_to_f16x4(q[k], h[2 * k], h[2 * k + 1]);
-          if constexpr (decltype(shifted)::value) {
-            const __half2 f = __float2half2_rn(pow2i((int)shift[i / HB / 2]));
+          if constexpr (SCALED) {
+            const __half2 f = __float2half2_rn(by[i / HB / 2]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), f);
@@ -276,16 +274,27 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
                          "r"(h[4 * c + 1]), "r"(h[4 * c + 2]), "r"(h[4 * c + 3])
                          : "memory");
         }
-      };
-      if (MIX && (shift[0] != 0.f || shift[1] != 0.f))
-        convert(std::true_type{});
-      else
-        convert(std::false_type{});
-      // generic stores before the tensor core's reads
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full_at(bar));
+        // generic stores before the tensor core's reads
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_at(bar));
+      }
+    };
+    // V's warps: whether any tile of this CTA needs it, found before the first tile (looked at
+    // in every tile it took 437 us where this takes 410, at 32 heads and blocks of 16)
+    bool scaled = false;
+    if (MIX && is_v) {
+      for (int g = 0; g < 4 * T; g += 32) {
+        const int key = key0 + (g + lane) * 16;
+        const float s = key < len && g + lane < 4 * T ? __ldg(A.vs + sc0 + (key >> A.blk_log2)) : 0.f;
+        scaled |= v_shift(v_exponent(s)) != 0.f;
+      }
+      scaled = __any_sync(0xffffffffu, scaled);
     }
+    if (MIX && scaled)
+      tiles(std::true_type{});
+    else
+      tiles(std::false_type{});
     cp_wait<0>();
   } else if (warp == NC) {
     if (lane == 0 && T > 0) {
@@ -448,13 +457,29 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
               if (!__all_sync(0xffffffffu, mbar_wait(pv_done(j - 1), par(j - 1), abort_flag, status)))
                 return false;
               tc_fence_after();
+              if constexpr (HD == 128) {  // in the scores' registers, which are read again
 #pragma unroll 1
-              for (int c = 0; c < HD; c += 16) {
-                float o[16];
-                tmem_ld16(tO + lane_off + c, o);
+                for (int c = 0; c < HD; c += 64) {
+                  tmem_ld32_nowait(tO + lane_off + c, s);
+                  tmem_ld32_nowait(tO + lane_off + c + 32, s + 32);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                tmem_st16(tO + lane_off + c, reinterpret_cast<const uint32_t*>(o));
+                  for (int i = 0; i < 64; ++i) s[i] *= alpha;
+                  tmem_st32(tO + lane_off + c, reinterpret_cast<const uint32_t*>(s));
+                  tmem_st32(tO + lane_off + c + 32, reinterpret_cast<const uint32_t*>(s) + 32);
+                }
+                tmem_ld32_nowait(tS(j) + lane_off, s);
+                tmem_ld32_nowait(tS(j) + lane_off + 32, s + 32);
+                tmem_wait_ld();
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 16) {
+                  float o[16];
+                  tmem_ld16(tO + lane_off + c, o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                  tmem_st16(tO + lane_off + c, reinterpret_cast<const uint32_t*>(o));
+                }
               }
             }
           }

@@ -55,8 +55,8 @@ def test_only_blocks_of_zeros(lib, rows):
 def weight_bound(q, K, V, vs):
     """One head: the output [R, hd] of q [R, hd] over K, V [n, hd] (vs [n]: V's scales) and a bound
     of its error before the store.  Weights come in tiles of 64 keys (16 where few rows ask).  With
-    the largest weight * scale of a tile brought to 2^-4 or more, f16 holds the others to half a
-    step, 2^-11 of each, or to 2^-25 where they are below 2^-14: 2^-21 of the largest.  Where a tile's scales span more than six
+    the largest weight * scale of a tile brought to 2^-6 or more, f16 holds the others to half a
+    step, 2^-11 of each, or to 2^-25 where they are below 2^-14: 2^-25 / 2^-6 = 2^-19 of the largest.  Where a tile's scales span more than six
     octaves its codes are first brought towards a common scale, by 2^-15 .. 2^7."""
     n, hd = K.shape
     s = q @ K.T / math.sqrt(hd)
@@ -69,12 +69,13 @@ def weight_bound(q, K, V, vs):
         e = np.log2(vs[t:t + 64])
         c = np.clip(e - e.max() + 7, -15, 7) if e.max() - e.min() > 6 else 0.0
         unit = 2.0 ** (e - c)
-        tol += 2.0 ** -21 * (p[:, t:t + 64] * unit).max(1, keepdims=True) * (np.abs(V[t:t + 64]) / unit[:, None]).sum(0)
+        tol += 2.0 ** -19 * (p[:, t:t + 64] * unit).max(1, keepdims=True) * (np.abs(V[t:t + 64]) / unit[:, None]).sum(0)
     return p @ V / l, tol / l, p @ np.abs(V) / l
 
 
 def check_weights(lib, q, cache, block, rows, where):
-    """Against the bound, which must itself be within 2^-10 of what the output is made of."""
+    """Against the bound, which must itself be within 2^-9 of what the output is made of: half of
+    what the store to bf16 may round."""
     k8, ks, v8, vs = cache
     B, N, H, hd = k8.shape
     o = torch.full_like(q, 7.0)
@@ -85,7 +86,7 @@ def check_weights(lib, q, cache, block, rows, where):
         one = lambda c, sc: decoded(c[b:b + 1, :, h:h + 1], sc[b:b + 1, h:h + 1], block)[0, :, 0]
         at = lambda t: f64(t.view(B, rows, H, hd)[b, :, h])
         ref, tol, size = weight_bound(at(q), one(k8, ks), one(v8, vs), f64(vs[b, h]).repeat(block)[:N])
-        assert np.all(tol <= 2.0 ** -10 * size)
+        assert np.all(tol <= 2.0 ** -9 * size)
         err = np.abs(at(o) - ref) - (tol + 2.0 ** -8 * (np.abs(ref) + tol))
         assert np.all(err <= 0), (b, h, err.max())
 
