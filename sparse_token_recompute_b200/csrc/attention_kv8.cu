@@ -456,14 +456,14 @@ __global__ void __launch_bounds__(RW * 32, 4)
 }
 
 // The shares of one output row, in share order: M = max m_s, w_s = l_s 2^(m_s - M),
-// O = sum w_s o_s / sum w_s.  WPR warps per (row, head), each with up to 8 shares whose
+// W = sum w_s, O = sum (w_s / W) o_s (no partial sum above the largest o_s).  WPR warps per (row, head), each with up to 8 shares whose
 // slices are on their way at once: bound by the latency of one such trip (one warp for 64
 // shares took 16 us of a call; eight warps for 12 shares and 1024 rows 3 us more than two).
 // An empty share has l = 0, and what its slice holds is dropped.
 template <int HD, int WPR>
 __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   constexpr int PER = HD / 32;
-  __shared__ float s_acc[WPR][HD + 1];
+  __shared__ float s_acc[WPR][HD];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -489,34 +489,31 @@ __global__ void __launch_bounds__(256) attn_kv8_merge_kernel(const Kv8Args A) {
   const float mx = warp_max(fmaxf(a.y != 0.f ? a.x : -INFINITY, b.y != 0.f ? b.x : -INFINITY));
   const float wa = a.y != 0.f ? a.y * exp2_approx(a.x - mx) : 0.f;
   const float wb = b.y != 0.f ? b.y * exp2_approx(b.x - mx) : 0.f;
-  float acc[PER], sum = 0.f;
+  float sum = warp_sum(wa + wb), acc[PER];
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float w = __shfl_sync(0xffffffffu, s0 < 32 ? wa : wb, (s0 + k) & 31);  // 0 past the last share
-    sum += w;
+    const float w = __shfl_sync(0xffffffffu, s0 < 32 ? wa : wb, (s0 + k) & 31) * inv;  // 0 past the last share
 #pragma unroll
     for (int x = 0; x < PER; ++x) acc[x] = fmaf(w, w != 0.f ? o[k][x] : 0.f, acc[x]);
   }
   if constexpr (WPR > 1) {
 #pragma unroll
     for (int x = 0; x < PER; ++x) s_acc[warp][lane * PER + x] = acc[x];
-    if (lane == 0) s_acc[warp][HD] = sum;
     __syncthreads();
     if (warp != 0) return;
 #pragma unroll
     for (int w = 1; w < WPR; ++w) {  // in share order
-      sum += s_acc[w][HD];
 #pragma unroll
       for (int x = 0; x < PER; ++x) acc[x] += s_acc[w][lane * PER + x];
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   __nv_bfloat16* dst = A.o + u * HD + lane * PER;
 #pragma unroll
   for (int i = 0; i < PER; i += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + i) = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+    *reinterpret_cast<__nv_bfloat162*>(dst + i) = __floats2bfloat162_rn(acc[i], acc[i + 1]);
   if (A.st_m && lane == 0) {
     float m = mx;
     normal_stats(m, sum);

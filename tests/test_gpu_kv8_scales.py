@@ -161,3 +161,21 @@ def test_every_block_has_a_channel_of_its_own(lib, rows, octaves, blocks, rising
     vs.copy_(torch.exp2(e - e.max() if rising else -e).expand_as(vs))
     q = normal((UNITS[0] * rows, UNITS[1] * hd), 3) * 0.1
     check_weights(lib, q.to(BF), many((k8, ks, v8, vs)), block, rows, WHERE)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40])
+@pytest.mark.parametrize("N", [100, 1000, 9000])
+def test_values_at_the_end_of_the_range(lib, rows, N):
+    """All V rows hold the largest values of bf16, so every mean is one of them: partial sums of
+    several warps and key shares stay inside the floats' range."""
+    hd, block = 128, 64
+    k8, ks, v8, vs = filled(lib, 1, N, 1, hd, block, 7)
+    want = torch.tensor([240.0, -240.0], device="cuda").repeat(hd // 2)   # 240 * 2^120 = 0.94 * 2^128
+    v8.copy_(want.to(torch.float8_e4m3fn).expand_as(v8))
+    vs.fill_(2.0 ** 120)
+    q = normal((rows, hd), 8).to(BF)
+    o = torch.zeros_like(q)
+    cnt = torch.tensor([rows], dtype=torch.int32, device="cuda")
+    lib.dllm_attention_kv8(q, k8, ks, v8, vs, o, cnt, rows, block)
+    # weights off by 2^-11, the sums' few steps, and the store
+    assert torch.all((o.double() / 2.0 ** 120 - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * 240)
