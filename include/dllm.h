@@ -146,7 +146,8 @@ typedef struct {
                          * as dllm_attention_stats_bf16), kept up to date by the updates */
   /* 8-bit caches (policy.kv8_block > 0): k and v point at e4m3 codes of the same shape;
    * HOST arrays of n_layers device pointers to their scales [B, n_kv_heads,
-   * ceil(N / kv8_block)] f32 (dllm_kv8_write); codes and scales start as zeros */
+   * ceil(N / kv8_block)] f32 (dllm_kv8_write); codes and scales start as zeros.
+   * Both NULL with policy.kv8_block 0 (DLLM_ERR_INVALID_ARG otherwise) */
   float* const* k_scale;
   float* const* v_scale;
 } dllm_cache;

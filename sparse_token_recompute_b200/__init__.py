@@ -30,7 +30,7 @@ if not os.path.exists(LIB_PATH):
 
 _lib = C.CDLL(LIB_PATH)
 
-DLLM_OK = 0
+DLLM_OK, DLLM_ERR_INVALID_ARG = 0, 1
 DLLM_F32, DLLM_BF16 = 0, 1
 DLLM_SCORE_COS, DLLM_SCORE_ES_L1 = 0, 1
 DLLM_SELECT_TOPK, DLLM_SELECT_THRESH = 0, 1
@@ -729,6 +729,7 @@ class Cache:
         dt = torch.bfloat16 if cfg.dtype == DLLM_BF16 else torch.float32
         kv = (B, N, cfg.n_kv_heads, cfg.head_dim)
         self.k_scale = self.v_scale = None
+        self.kv8_block = int(kv8_block)
         if kv8_block:
             layers = [kv8_cache(*kv, kv8_block, device) for _ in range(cfg.n_layers)]
             self.k, self.k_scale, self.v, self.v_scale = ([c[i] for c in layers] for i in range(4))
@@ -795,6 +796,13 @@ def dllm_partial_layer(cfg: ModelCfg, lw: LayerW, x_in, x_out, idx, count, k_cac
     _check(st, "dllm_partial_layer")
 
 
+def _same_block(cache: Cache, pol: Policy, where: str):
+    """An 8-bit cache steps under policies of its own block: another one's scales lie elsewhere."""
+    if cache.kv8_block and cache.kv8_block != pol.kv8_block:
+        raise DllmError(DLLM_ERR_INVALID_ARG, f"{where}: a cache with blocks of {cache.kv8_block} under "
+                                              f"policy.kv8_block {pol.kv8_block}")
+
+
 def dllm_step_workspace_size(cfg: ModelCfg, B: int, N: int, pol: Policy) -> int:
     return int(_step_ws(C.byref(cfg), B, N, C.byref(pol)))
 
@@ -803,6 +811,7 @@ def dllm_step(model: Model, cache: Cache, tokens, pol: Policy, dense: bool, ws: 
               forced_idx=None, forced_count=None, forced_unmask_pos=None, idx_out=None,
               count_out=None, pos_out=None, scores_out=None, stream=None):
     B, N = tokens.shape
+    _same_block(cache, pol, "dllm_step")
     st = _step(C.byref(model.cfg), C.byref(model.s), C.byref(cache.s), ptr(tokens), B, N,
                C.byref(pol), int(bool(dense)), ptr(forced_idx), ptr(forced_count),
                ptr(forced_unmask_pos), ptr(idx_out), ptr(count_out), ptr(pos_out),
@@ -819,6 +828,7 @@ def dllm_generate(model: Model, cache: Cache, tokens, pol: Policy, n_steps: int,
     """n_steps steps with the policy's refresh schedule; returns the per-step
     dense flags (host list of bool).  pos_log: device [n_steps, B, capacity]."""
     B, N = tokens.shape
+    _same_block(cache, pol, "dllm_generate")
     flags = (C.c_uint8 * max(int(n_steps), 1))()
     st = _gen(C.byref(model.cfg), C.byref(model.s), C.byref(cache.s), ptr(tokens), B, N,
               C.byref(pol), int(n_steps), ptr(pos_log), flags, ws.ptr, ws.nbytes,
@@ -834,6 +844,7 @@ def dllm_step_ex(model: Model, cache: Cache, tokens, pol: Policy, dense: bool, w
     scores_out, forced_idx2, forced_count2, idx2_out, count2_out, scores2_out,
     ffn_rows_out, forced_ffn)."""
     B, N = tokens.shape
+    _same_block(cache, pol, "dllm_step_ex")
     s = StepIO(*[ptr(io.get(name)) for name, _ in StepIO._fields_])
     unknown = set(io) - {name for name, _ in StepIO._fields_}
     if unknown:
@@ -856,6 +867,7 @@ def dllm_step_host(model: Model, cache: Cache, tokens_host, pol: Policy, dense: 
     tokens_host [B, N] int32 and pos_host [B, capacity] int32: CPU tensors,
     preferably pinned."""
     B, N = tokens_host.shape
+    _same_block(cache, pol, "dllm_step_host")
     st = _step_host(C.byref(model.cfg), C.byref(model.s), C.byref(cache.s), ptr(tokens_host), B,
                     N, C.byref(pol), int(bool(dense)), ptr(pos_host), ws.ptr, ws.nbytes,
                     _stream(stream))

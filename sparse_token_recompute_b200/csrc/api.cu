@@ -1116,6 +1116,8 @@ extern "C" dllm_status dllm_step_ex(const dllm_model_cfg* c, const dllm_model_w*
       if (!cache->k_scale[l] || !cache->v_scale[l] || !aligned(cache->k_scale[l], 4) ||
           !aligned(cache->v_scale[l], 4))
         return DLLM_ERR_INVALID_ARG;
+  } else if (cache->k_scale || cache->v_scale) {
+    return DLLM_ERR_INVALID_ARG;  // codes, which a step over plain caches would overrun
   }
   const int l2 = pol->score_layer2;
   if (l2 != 0) {
