@@ -341,12 +341,20 @@ def dllm_selftest_gemm_stall(A, Bm, Cm, ws: Workspace = None, stream=None):
     return ws
 
 
+def _no_codes(where: str, *tensors):
+    """The calls over plain K/V: one-byte codes (kv8_cache) would be read past their end."""
+    for t in tensors:
+        if t.element_size() == 1:
+            raise TypeError(f"{where}: K/V of {t.dtype}, wanted rows of the model's dtype")
+
+
 def dllm_attention_workspace_size(B: int) -> int:
     return int(_attn_ws(B))
 
 
 def dllm_attention_bf16(q, k_cache, v_cache, o, count, k_cap: int, ws: Workspace = None,
                         stream=None):
+    _no_codes("dllm_attention_bf16", k_cache, v_cache)
     B, N, Hkv, hd = k_cache.shape
     Hq = q.shape[1] // hd
     if ws is None:
@@ -360,6 +368,7 @@ def dllm_attention_bf16(q, k_cache, v_cache, o, count, k_cap: int, ws: Workspace
 def dllm_attention_stats_bf16(q, k_cache, v_cache, o, m, l, count, k_cap: int,
                               ws: Workspace = None, stream=None):
     """dllm_attention_bf16 plus each row's softmax statistics m, l [B*k_cap, Hq] (f32)."""
+    _no_codes("dllm_attention_stats_bf16", k_cache, v_cache)
     B, N, Hkv, hd = k_cache.shape
     Hq = q.shape[1] // hd
     if ws is None:
@@ -375,6 +384,7 @@ def dllm_attention_update_bf16(q, o, m, l, r_count, r_cap: int, k_new, v_new, k_
                                stream=None):
     """Incremental attention of stable rows (see include/dllm.h); q/o [B*r_cap, Hq*hd],
     m/l [B*r_cap, Hq] updated in place; changed keys [B*a_cap, Hkv, hd]."""
+    _no_codes("dllm_attention_update_bf16", k_new, v_new, k_old, v_old)
     B = r_count.shape[0]
     hd = k_new.shape[-1]
     Hq = q.shape[1] // hd
@@ -394,6 +404,7 @@ def dllm_attention_bf16_noalloc(q, k_cache, v_cache, o, count, k_cap: int, strea
     """Partial attention without a workspace, for callers that cannot allocate
     device memory (memory carved into fixed pools, operators handed only their
     tensors); its scratch is a fixed array inside the library shared by all calls."""
+    _no_codes("dllm_attention_bf16_noalloc", k_cache, v_cache)
     B, N, Hkv, hd = k_cache.shape
     Hq = q.shape[1] // hd
     st = _attn_noalloc(ptr(q), ptr(k_cache), ptr(v_cache), ptr(o), ptr(count), B, int(k_cap), N,
@@ -788,6 +799,7 @@ def dllm_partial_layer_workspace_size(cfg: ModelCfg, B: int, N: int, k_cap: int)
 
 def dllm_partial_layer(cfg: ModelCfg, lw: LayerW, x_in, x_out, idx, count, k_cache, v_cache,
                        ws: Workspace, x_in_is_full: bool, stream=None):
+    _no_codes("dllm_partial_layer", k_cache, v_cache)
     B, k_cap = idx.shape
     N = k_cache.shape[1]
     st = _layer(C.byref(cfg), C.byref(lw), ptr(x_in), int(bool(x_in_is_full)), ptr(x_out),

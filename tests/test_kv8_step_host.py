@@ -51,3 +51,23 @@ def test_scales_without_a_block_are_refused_by_the_library(lib):  # noqa: F811
     cache.v_scale = None
     cache._refresh()
     assert go() == INVALID
+
+
+def test_codes_are_not_a_cache_of_the_other_calls(lib):  # noqa: F811
+    """Layer and attention calls over plain caches read two or four bytes per element."""
+    import sparse_token_recompute_b200 as S
+    model, pol, cache, ws, tokens = case(S, 64, 64)
+    B, N = tokens.shape
+    k8, v8 = cache.k[0], cache.v[0]
+    q = torch.zeros(B * 4, 256, dtype=torch.bfloat16)
+    x, o = torch.zeros_like(cache.h_ref), torch.zeros_like(q)
+    idx, cnt = torch.zeros(B, 4, dtype=torch.int32), torch.ones(B, dtype=torch.int32)
+    ml = torch.zeros(B * 4, 4)
+    for a, b in ((k8, v8), (k8.view(torch.uint8), v8), (v8.to(torch.bfloat16), v8)):
+        for go in (lambda: S.dllm_partial_layer(model.cfg, model.layer(0), x, o, idx, cnt, a, b, ws, True, stream=0),
+                   lambda: S.dllm_attention_bf16(q, a, b, o, cnt, 4, ws=ws, stream=0),
+                   lambda: S.dllm_attention_stats_bf16(q, a, b, o, ml, ml, cnt, 4, ws=ws, stream=0),
+                   lambda: S.dllm_attention_bf16_noalloc(q, a, b, o, cnt, 4, stream=0),
+                   lambda: S.dllm_attention_update_bf16(q, o, ml, ml, cnt, 4, a, b, a, b, cnt, 4, 2, ws=ws, stream=0)):
+            with pytest.raises(TypeError):
+                go()
