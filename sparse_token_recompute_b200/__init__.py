@@ -18,8 +18,6 @@ import operator
 import os
 from typing import Dict, List, Optional, Sequence
 
-import torch
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdllm.so")
 
@@ -35,6 +33,18 @@ DLLM_F32, DLLM_BF16 = 0, 1
 DLLM_SCORE_COS, DLLM_SCORE_ES_L1 = 0, 1
 DLLM_SELECT_TOPK, DLLM_SELECT_THRESH = 0, 1
 DLLM_DEV_TIMEOUT, DLLM_DEV_CAPACITY, DLLM_DEV_BAD_INDEX, DLLM_DEV_BAD_SHAPE = 1, 2, 4, 8
+
+
+class _Torch:
+    """Stands for torch until a call needs it: structures, sizes and plans do without."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 vp = C.c_void_p
 
@@ -209,7 +219,6 @@ def _dtype_code(t) -> int:
 # ----------------------------------------------------------------- workspace
 
 def _empty_bytes(nbytes: int, device):
-    import torch
     # 256-byte alignment: torch's caching allocator returns at least 512-byte aligned blocks
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -442,8 +451,14 @@ def _bad(checks, device):
     raise ValueError("arguments that do not fit together")
 
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
-_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+_CODES = _F32 = _I32 = _BF16 = None
+
+
+def _dtypes():
+    """The types above, which the calls below compare with (set by the first of them)."""
+    global _CODES, _F32, _I32, _BF16
+    _CODES = (torch.float8_e4m3fn, torch.uint8)
+    _F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
 
 
 def _kv8_checks(k8, k_scale, v8, v_scale, B, N, H, hd, nblk):
@@ -525,6 +540,8 @@ def _launch(dev: int, fn, args, ws, stream, where: str):
 
 def dllm_rope_table(table, theta: float, stream=None):
     """table [N, head_dim/2, 2] float32 <- cos, sin of the rotation angles."""
+    if _F32 is None:
+        _dtypes()
     dev = table.get_device()
     if (table.dtype is not _F32 or dev < 0 or table.dim() != 3 or table.shape[2] != 2
             or not table.is_contiguous()):
@@ -542,6 +559,8 @@ def dllm_qk_norm_rope(q, k, q_gain, k_gain, rope, q_out, k_out, idx, count, eps:
     [B, N, n_kv_heads, head_dim] cache whose rows at the positions are meant; rope: a
     dllm_rope_table or None; idx [B, k_cap] and count [B] as for dllm_partial_layer.  The
     number of positions N comes from a cache or the table."""
+    if _F32 is None:
+        _dtypes()
     code, dt, dev, hd = _dtype_code(q), q.dtype, q.get_device(), q_gain.shape[0]
     if idx is None and count is None:
         raise ValueError("idx or count: the number of sequences is theirs")
@@ -606,6 +625,8 @@ def kv8_cache(B: int, N: int, n_kv_heads: int, head_dim: int, block: int, device
 
 
 def _kv8_rows_call(fn, where, k, v, idx, count, k8, k_scale, v8, v_scale, block, ws, stream, reads):
+    if _F32 is None:
+        _dtypes()
     shape = k8.shape
     B, N, H, hd = shape
     nblk, dev, w = -(-N // max(block, 1)), k8.get_device(), H * hd
@@ -650,6 +671,8 @@ def dllm_attention_kv8(q, k8, k_scale, v8, v_scale, o, count, k_cap: int, block:
     """Attention of compact query rows [B*k_cap, n_heads*head_dim] over the 8-bit cache (the
     first kv_len[b] positions of each sequence); returns the workspace, to be kept for the
     next call of these sizes."""
+    if _F32 is None:
+        _dtypes()
     bf16, shape, dev = _BF16, k8.shape, k8.get_device()
     B, N, H, hd = shape
     R, wq = q.shape
@@ -899,7 +922,6 @@ class StepGraph:
 
     def __init__(self, model: Model, cache: Cache, tokens, pol: Policy, ws: Workspace,
                  dense: bool = False, pos_out=None):
-        import torch
         profile_enable(False)  # per-launch timing events cannot be read back from a graph
         self.stream = torch.cuda.Stream()
         self.graph = torch.cuda.CUDAGraph()
