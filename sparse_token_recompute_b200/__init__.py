@@ -568,6 +568,8 @@ def dllm_qk_norm_rope(q, k, q_gain, k_gain, rope, q_out, k_out, idx, count, eps:
     wq, sk = q.shape[1], k.shape
     k_in, k_to = len(sk) == 4, k_out.dim() == 4
     if N is None:
+        if rope is None and not (k_in or k_to):
+            raise ValueError("N: the number of positions, which neither a cache nor a table gives")
         N = sk[1] if k_in else k_out.shape[1] if k_to else rope.shape[0]
     wk = sk[2] * hd if k_in else sk[1]
     rows, ldq = _rows_fit(q, dt, wq, dev)
