@@ -68,14 +68,16 @@ __device__ __forceinline__ float near_inverse(float s) {
   constexpr float lo = 1.0f / (1 << kKv8Far), hi = 1 << kKv8Far;
   return s >= lo && s <= hi ? kv8_inverse(s) : 0.f;
 }
-// whether a tile whose largest x_j lies d above the reference wants another one
-__device__ __forceinline__ bool wants_ref(float d) {
-  return fabsf(d - 0.5f * (kKv8High + kKv8Low)) > 0.5f * (kKv8High - kKv8Low);
+// whether a tile whose largest x_j lies d above the reference wants another one; mixed: a
+// tile of several V scales far apart, whose largest weight is to be 2^8 .. 2^15
+__device__ __forceinline__ bool wants_ref(float d, bool mixed = false) {
+  const float lo = mixed ? 8.f : kKv8Low;
+  return fabsf(d - 0.5f * (kKv8High + lo)) > 0.5f * (kKv8High - lo);
 }
 // moves the reference m to the tile's largest x_j, mx, but not below `low`; false: it stays
-__device__ __forceinline__ bool new_ref(float mx, float& m, float& low) {
-  if (!wants_ref(mx - m) || !(mx > low - kKv8Lost) || (mx < m && m <= low)) return false;
-  m = fmaxf(mx - kKv8Aim, low);
+__device__ __forceinline__ bool new_ref(float mx, float& m, float& low, bool mixed = false) {
+  if (!wants_ref(mx - m, mixed) || !(mx > low - kKv8Lost) || (mx < m && m <= low)) return false;
+  m = fmaxf(mx - (mixed ? 12.f : kKv8Aim), low);
   low = fmaxf(low, m - kKv8Fall);
   return true;
 }

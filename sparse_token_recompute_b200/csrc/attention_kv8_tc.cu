@@ -20,12 +20,13 @@
 //
 // Bound by shared memory: per 64 keys a CTA moves 128 KB through it (codes in and
 // out 32, f16 tiles 32, Q and K for Q K^T 48, V 16) = 1024 cycles at 128 bytes a
-// cycle.  32 sequences x 308 rows x 1536 keys, 32 heads of 128: over 8 kv heads 347 us
-// (714 TFLOP/s; the kernel over a bf16 cache 380), over 32, where the third of each
-// sequence's tiles holds 52 of 128 rows, 407.  Before, at the latter: scores read twice
-// and 128 keys 696 us; codes through registers and L1 540; K and V converted in turn by
-// the same warps 445 (381 over 8 kv heads).  Two row tiles per CTA over the same keys, one
-// CTA per SM, 378 us at 256 rows against 350; codes by TMA 468 against 441.
+// cycle.  32 sequences x 308 rows x 1536 keys, 32 heads of 128: over 8 kv heads 346 us
+// (716 TFLOP/s; the kernel over a bf16 cache 346), over 32, where the third of each
+// sequence's tiles holds 52 of 128 rows, 401 (358); under the power cap, at 1.78 GHz, 445.
+// Dropped on the way, at the latter: scores read twice and 128 keys 696 us; codes through
+// registers and L1 540; K and V converted in turn by the same warps 445.  Two row tiles per
+// CTA over the same keys, one CTA per SM, 378 us at 256 rows against 350; codes by TMA 468
+// against 441.
 // Every mbarrier wait is bounded; a timeout sets DLLM_DEV_TIMEOUT, drains the MMAs,
 // frees TMEM and returns.
 #include <type_traits>
@@ -68,7 +69,8 @@ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// MIX: blocks shorter than a tile of keys, whose V scales may differ within it
+// MIX: blocks shorter than a tile of keys, whose V scales may differ within it (407 us where
+// blocks of 64 take 401)
 template <int HD, bool MIX>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args A) {
   using L = Smem<HD>;
@@ -215,16 +217,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
   if (warp < NC) {
     // ---------------------------------------------------------------- converters
     // Blocks shorter than a tile: where the V scales of a tile span more than six octaves, the
-    // codes themselves are brought towards a common scale, as far as f16 holds them exactly
-    // (their last bit is 2^-9, the largest 448: by 2^-15 .. 2^7), so that the weights' range
-    // is not spent on it.  Exponent of the factor of lane's (0 .. 3) group of 16 keys.
-    auto v_shift = [&](float e) {
+    // codes themselves are brought towards a common scale, by 2^-7 .. 2^1 (f16 would hold them
+    // from 2^-15 to 2^7, but keys of a small block may weigh more, and then it is the scales'
+    // difference that keeps their weights and the others' in range), and the largest weight
+    // to 2^8 or more.  Exponent of the factor of lane's (0 .. 3) group of 16 keys.
+    auto v_shift = [&](float e, bool& mixed) {
       float hi = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
       float lo = e == -INFINITY ? INFINITY : e;
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
-      return hi - lo > 6.f ? fminf(fmaxf(e - hi + 7.f, -15.f), 7.f) : 0.f;
+      mixed |= hi - lo > 6.f;
+      return hi - lo > 6.f ? fminf(fmaxf(e - hi + 1.f, -7.f), 1.f) : 0.f;
     };
     auto tiles = [&](auto scaled) {
       constexpr bool SCALED = decltype(scaled)::value;
@@ -233,15 +237,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
         float by[2];  // the factors of this warp's two groups
         if constexpr (SCALED) {
           if (!mbar_wait(sc_full(j), (j / NSC) & 1, abort_flag, status)) return;
-          by[0] = scales[j % NSC * 4 + (warp & 1) * 2].w;
-          by[1] = scales[j % NSC * 4 + (warp & 1) * 2 + 1].w;
+          by[0] = fabsf(scales[j % NSC * 4 + (warp & 1) * 2].w);
+          by[1] = fabsf(scales[j % NSC * 4 + (warp & 1) * 2 + 1].w);
         } else if (!is_v && warp == (j & 1)) {
-          const float e = v_exponent(sc.y), c = MIX ? v_shift(e) : 0.f;
+          bool mixed = false;
+          const float e = v_exponent(sc.y), c = MIX ? v_shift(e, mixed) : 0.f;
           const float inv = near_inverse(sc.y) * (MIX ? pow2i((int)c) : 1.f);
           // (the sum takes the whole tile one way: a far scale makes it far)
           const bool near = __all_sync(0xffffffffu, lane >= 4 || key0 + j * BK + lane * 16 >= len || inv != 0.f);
           if (lane < 4)
-            scales[j % NSC * 4 + lane] = make_float4(sc.x, e - c, near ? inv : 0.f, MIX ? pow2i((int)c) : 1.f);
+            scales[j % NSC * 4 + lane] = make_float4(sc.x, e - c, near ? inv : 0.f, mixed ? -pow2i((int)c) : 1.f);
           __syncwarp();
           if (lane == 0) mbar_arrive(sc_full(j));
           sc = fetch_scales(j + 2);
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
       for (int g = 0; g < 4 * T; g += 32) {
         const int key = key0 + (g + lane) * 16;
         const float s = key < len && g + lane < 4 * T ? __ldg(A.vs + sc0 + (key >> A.blk_log2)) : 0.f;
-        scaled |= v_shift(v_exponent(s)) != 0.f;
+        v_shift(v_exponent(s), scaled);
       }
       scaled = __any_sync(0xffffffffu, scaled);
     }
@@ -447,9 +452,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
             const float2 f = *reinterpret_cast<const float2*>(sc + g);
             if (!LAST || 16 * g < nkeys) mx = fmaxf(mx, fmaf(fmaxf(a, c), rs * f.x, f.y));
           }
-          if (__any_sync(0xffffffffu, wants_ref(mx - m))) {
+          const bool mixed = MIX && sc[0].w < 0.f;
+          if (__any_sync(0xffffffffu, wants_ref(mx - m, mixed))) {
             const float before = m;
-            const bool move = new_ref(mx, m, low);
+            const bool move = new_ref(mx, m, low, mixed);
             const float alpha = move ? exp2_approx(before - m) : 1.f;  // the first time: 0
             if (move) raise_sum(sc[0].z != 0.f ? m - sc[0].y : lm);
             if (j > 0 && __any_sync(0xffffffffu, move)) {
