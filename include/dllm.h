@@ -577,7 +577,10 @@ size_t dllm_kv8_scale_count(int B, int N, int n_kv_heads, int block);
  * NaN.  Where the scale changed, the block's other positions are re-encoded at
  * it (exactly, but for bits below e4m3's smallest step 2^-9), or zeroed if
  * the block held no rows.  Blocks without new rows are untouched; a call that
- * is repeated changes nothing.  k, v: compact rows of n_kv_heads*head_dim
+ * is repeated changes nothing.  A scale falls only where a call writes the
+ * whole block: under one that is 2^k larger than its rows need, values below
+ * 2^(k-14) of the largest lose bits, and from k = 19 on all are stored as zeros.
+ * k, v: compact rows of n_kv_heads*head_dim
  * bf16, strides multiples of 8, 16-byte aligned; head_dim 64 or 128.
  */
 dllm_status dllm_kv8_write(const void* k, int ldk, const void* v, int ldv, const int32_t* idx,
@@ -603,6 +606,9 @@ dllm_status dllm_kv8_read(const void* k8, const float* k_scale, const void* v8,
  * m, l: both NULL, or [B*k_cap, n_heads] f32 softmax statistics as
  * dllm_attention_stats_bf16 returns them, here with 1 <= l < 2 (-inf and 0
  * without keys).  B * k_cap * n_heads < 2^31.
+ * Weights are f16, of 11 bits: each is off by 2^-11 of itself, or, where that
+ * is more, weight * V scale by 2^-19 of the largest such product among the 64
+ * neighbouring keys of its tile.  Sums are fp32 and do not depend on the scales.
  * ws: dllm_attention_kv8_workspace_size() bytes; calls that may overlap need a
  * workspace each.
  */

@@ -13,7 +13,7 @@
 //   queries a bf16 row times the power of two that brings its largest element
 //           to [2^14, 2^15): 8 bits fit f16's 11, and elements down to 2^-28
 //           of the largest stay normal numbers;
-//   P       exp2(score - reference), rounded to f16's 11 bits (bf16 would keep 8).
+//   P       2^(x_j - r), see below, rounded to f16's 11 bits (bf16 would keep 8).
 // The K scale multiplies the fp32 score.  The V scale 2^e of a key's block is an
 // addend of its exponent: with x_j = score_j + e_j (log2 units) and a reference r,
 //   O = sum_j 2^(x_j - r) v8_j,   l = sum_j 2^(score_j - r'),   out = O / l * 2^(r - r').
@@ -24,7 +24,7 @@
 // down, such that each tile's largest weight is 2^-6 .. 2^15 in f16; O, in fp32, is rescaled
 // where r moves.  A weight is then off by at most 2^-11 of itself, or 2^-19 of the largest
 // weight * scale of its own tile: 16 keys here, 64 of the tcgen05 kernel, which also brings
-// the codes of a tile of several blocks towards one scale.  r falls by 2^64 at most; tiles
+// the codes of a tile of several blocks towards one scale if theirs lie far apart.  r falls by 2^64 at most; tiles
 // below that lose bits from 2^-83 of the largest weight * scale on.
 //
 // The sum has a reference r' of its own, near the largest score, and takes a weight as
@@ -52,9 +52,10 @@ __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0
 // ---------------------------------------------------------------- few query rows
 
 // Packed query rows per (sequence, kv head) that still run here: one tile of RM.  At 1 row
-// and 32 x 1536 keys, 32 heads over 32, 73 us against the tcgen05 kernel's 118; at 20 rows
-// over 8 heads 9.6 against 10.5 (1 x 1536 keys) and 25.2 against 20.5 (1 x 16384); at 64
-// rows 36.9 against 30.3 (16 x 1536) and 316 against 180 (64 x 4096).
+// and 32 x 1536 keys, 32 heads over 32, 75 us against the tcgen05 kernel's 122; at 16 rows
+// of 1 x 1536 keys over 8 heads 7.8 against 10.3.  At 20 rows over 8 heads 11.5 against 10.6
+// (1 x 1536 keys) and 25 against 23 (1 x 16384); at 64 rows 39 against 30.5 (16 x 1536) and
+// 317 against 180 (64 x 4096).
 constexpr int kKv8TcRows = 16;
 constexpr int RW = 4;        // warps per CTA
 constexpr int RM = 16;       // packed query rows per CTA
@@ -83,8 +84,8 @@ struct RowsSmem {
 // order of the inner index that Q's fragments share; V by gathering one byte of two
 // keys.  With so few rows the tensor cores' rate does not matter and the kernel is
 // bound by the codes' way: 2 bytes per key and head_dim element.  32 sequences x 1 row x
-// 1536 keys, 32 heads of 128 over 32 (403 MB): 73 us, 5.5 TB/s; 1 x 1 x 16384 keys (134
-// MB) 31 us, start-up and merge included.
+// 1536 keys, 32 heads of 128 over 32 (403 MB): 75 us, 5.4 TB/s; 1 x 1 x 16384 keys (134
+// MB) 32 us, start-up and merge included.
 template <int HD>
 __global__ void __launch_bounds__(RW * 32, 4)
     attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

@@ -6,9 +6,11 @@
 // stands for c * scale.  Scales are powers of two: a decoded value has the
 // code's 4 significant bits, so it is exact in bf16, and a row that is
 // re-encoded because its block's scale grew keeps every bit except those that
-// fall below e4m3's smallest step.  e4m3 is a floating format, so a scale up
-// to twice (or many times) the tight one costs no precision above 2^-14 of
-// the block's largest value.
+// fall below e4m3's smallest step.  e4m3 is a floating format (normal from 2^-6
+// to 448): under the tight scale the values down to 2^-14 of the block's
+// largest keep their 4 bits, under one 2^k too large those down to 2^(k-14),
+// and from k = 19 on every value rounds to zero.  A scale falls only where
+// the whole block is written.
 #pragma once
 
 #include <cuda_fp16.h>

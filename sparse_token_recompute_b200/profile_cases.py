@@ -8,7 +8,12 @@ but a few GB at most, runs the kernel `--warmup` times untimed and then
   python -m sparse_token_recompute_b200.profile_cases score --B 32 --L 1024 --d 4096
   python -m sparse_token_recompute_b200.profile_cases layer --B 32 --N 1536 --k 308
   python -m sparse_token_recompute_b200.profile_cases attention --B 32 --N 1536 --k 308
+  python -m sparse_token_recompute_b200.profile_cases attention_kv8 --B 32 --N 1536 --k 1 --kv-heads 8
+  python -m sparse_token_recompute_b200.profile_cases write_kv8 --B 32 --N 1536 --k 308
+  python -m sparse_token_recompute_b200.profile_cases read_kv8 --B 32 --N 1536 --k 1536
+  python -m sparse_token_recompute_b200.profile_cases qk_norm --B 32 --N 1536 --k 308
   python -m sparse_token_recompute_b200.profile_cases step --B 1 --ratio 0.10
+  python -m sparse_token_recompute_b200.profile_cases step --B 32 --ratio 0.20 --kv8-block 64
   python -m sparse_token_recompute_b200.profile_cases step_graph --B 1 --ratio 0.10
 """
 from __future__ import annotations
@@ -84,6 +89,58 @@ def case_attention(a):
             "kv_bytes": 2 * a.B * a.N * a.kv_heads * hd * 2}
 
 
+def _kv8_inputs(a):
+    """A filled 8-bit cache (one scale throughout, as rows of one size give) and row lists."""
+    hd, nblk = 128, -(-a.N // a.kv8_block)
+    code = lambda i: (SY.normal((a.B, a.N, a.kv_heads, hd), 100.0, i, "cuda", "f32").clamp_(-448, 448)
+                      .to(torch.float8_e4m3fn))
+    scale = lambda: torch.full((a.B, a.kv_heads, nblk), 2.0 ** -6, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    idx = torch.sort(torch.rand(a.B, a.N, generator=g, device="cuda").argsort(1)[:, :a.k], 1)[0]
+    cnt = torch.full((a.B,), a.k, dtype=torch.int32, device="cuda")
+    return (code(2), scale(), code(3), scale()), idx.to(torch.int32).contiguous(), cnt
+
+
+def case_attention_kv8(a):
+    """case_attention over an 8-bit cache."""
+    H, hd = a.heads, 128
+    cache, _, cnt = _kv8_inputs(a)
+    q = SY.normal((a.B * a.k, H * hd), 1.0, 1, "cuda", "bf16")
+    o = torch.empty_like(q)
+    ws = S.dllm_attention_kv8(q, *cache, o, cnt, a.k, a.kv8_block)
+    ms = _time(lambda: S.dllm_attention_kv8(q, *cache, o, cnt, a.k, a.kv8_block, ws=ws), a.warmup, a.iters)
+    return {"case": "attention_kv8", "ms": ms, "tflops": 4.0 * a.B * a.k * a.N * H * hd / ms / 1e9,
+            "kv_bytes": 2 * a.B * a.N * a.kv_heads * hd}
+
+
+def case_write_kv8(a):
+    """New K/V rows of one layer into its 8-bit cache (all of them with --k N)."""
+    cache, idx, cnt = _kv8_inputs(a)
+    k, v = (SY.normal((a.B * a.k, a.kv_heads * 128), 1.0, i, "cuda", "bf16") for i in (4, 5))
+    ms = _time(lambda: S.dllm_kv8_write(k, v, idx, cnt, *cache, a.kv8_block), a.warmup, a.iters)
+    return {"case": "write_kv8", "ms": ms, "GBps": 3 * 2 * k.numel() / ms / 1e6}
+
+
+def case_read_kv8(a):
+    """Rows of one layer's 8-bit cache back to bf16."""
+    cache, idx, cnt = _kv8_inputs(a)
+    k, v = (torch.empty(a.B * a.k, a.kv_heads * 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ms = _time(lambda: S.dllm_kv8_read(*cache, idx, cnt, k, v, a.kv8_block), a.warmup, a.iters)
+    return {"case": "read_kv8", "ms": ms, "GBps": 3 * 2 * k.numel() / ms / 1e6}
+
+
+def case_qk_norm(a):
+    """q/k norm and rotation of one layer's selected rows."""
+    hd = 128
+    _, idx, cnt = _kv8_inputs(a)
+    q, k = (SY.normal((a.B * a.k, h * hd), 1.0, i, "cuda", "bf16") for i, h in ((1, a.heads), (2, a.kv_heads)))
+    g, rope = torch.ones(hd, dtype=torch.bfloat16, device="cuda"), torch.empty(a.N, hd // 2, 2, device="cuda")
+    S.dllm_rope_table(rope, 5e5)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    ms = _time(lambda: S.dllm_qk_norm_rope(q, k, g, g, rope, qo, ko, idx, cnt, 1e-5), a.warmup, a.iters)
+    return {"case": "qk_norm", "ms": ms, "GBps": 4 * (q.numel() + k.numel()) / ms / 1e6}
+
+
 def case_attention_update(a):
     """Incremental attention of the stable rows of one 8B layer: B sequences, N - k
     stable rows each, k changed keys each (the rows the step recomputed)."""
@@ -118,13 +175,14 @@ def case_step(a):
     W = SY.model_weights(shape, seed=0, device="cuda")
     model = S.Model(S.cfg_from_shape(shape), W)
     tokens = SY.prompt_tokens(shape, seed=1, device="cuda")
-    cache = S.Cache(model.cfg, shape.batch, shape.seq_len)
+    cache = S.Cache(model.cfg, shape.batch, shape.seq_len, kv8_block=a.kv8_block)
     pol = S.make_policy(0, shape.alpha, 0, 0, shape.k, 0.0, shape.n_unmask, shape.prompt_len,
-                        shape.block_len)
+                        shape.block_len, kv8_block=a.kv8_block)
     ws = S.Workspace(S.dllm_step_workspace_size(model.cfg, shape.batch, shape.seq_len, pol))
     S.dllm_step(model, cache, tokens, pol, True, ws)
     ms = _time(lambda: S.dllm_step(model, cache, tokens, pol, False, ws), a.warmup, a.iters)
-    return {"case": "step", "B": shape.batch, "N": shape.seq_len, "k": shape.k, "ms": ms}
+    return {"case": "step", "B": shape.batch, "N": shape.seq_len, "k": shape.k,
+            "kv8_block": a.kv8_block, "ms": ms}
 
 
 def case_step_graph(a):
@@ -135,15 +193,16 @@ def case_step_graph(a):
     W = SY.model_weights(shape, seed=0, device="cuda")
     model = S.Model(S.cfg_from_shape(shape), W)
     tokens = SY.prompt_tokens(shape, seed=1, device="cuda")
-    cache = S.Cache(model.cfg, shape.batch, shape.seq_len)
+    cache = S.Cache(model.cfg, shape.batch, shape.seq_len, kv8_block=a.kv8_block)
     pol = S.make_policy(0, shape.alpha, 0, 0, shape.k, 0.0, shape.n_unmask, shape.prompt_len,
-                        shape.block_len)
+                        shape.block_len, kv8_block=a.kv8_block)
     ws = S.Workspace(S.dllm_step_workspace_size(model.cfg, shape.batch, shape.seq_len, pol))
     S.dllm_step(model, cache, tokens, pol, True, ws)
     S.dllm_step(model, cache, tokens, pol, False, ws)
     graph = S.StepGraph(model, cache, tokens, pol, ws)
     ms = _time(graph.replay, a.warmup, a.iters)
-    return {"case": "step_graph", "B": shape.batch, "N": shape.seq_len, "k": shape.k, "ms": ms}
+    return {"case": "step_graph", "B": shape.batch, "N": shape.seq_len, "k": shape.k,
+            "kv8_block": a.kv8_block, "ms": ms}
 
 
 def case_layer(a):
@@ -170,7 +229,8 @@ def case_layer(a):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["gemm", "score", "layer", "attention", "attention_update",
-                                     "step", "step_graph"])
+                                     "attention_kv8", "write_kv8", "read_kv8", "qk_norm", "step",
+                                     "step_graph"])
     ap.add_argument("--ratio", type=float, default=0.10)
     ap.add_argument("--heads", type=int, default=32)
     ap.add_argument("--kv-heads", dest="kv_heads", type=int, default=32)
@@ -185,16 +245,23 @@ def main():
     ap.add_argument("--Mm", type=int, default=256)
     ap.add_argument("--k", type=int, default=None,
                     help="rows per sequence (default 256 for score, 308 for layer/attention)")
+    ap.add_argument("--kv8-block", dest="kv8_block", type=int, default=None,
+                    help="positions per scale of an 8-bit cache (64; for a step 0: caches of its dtype)")
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--iters", type=int, default=3)
     a = ap.parse_args()
+    rows = ("layer", "attention", "attention_update", "attention_kv8", "write_kv8", "read_kv8", "qk_norm")
     if a.k is None:
-        a.k = 308 if a.case in ("layer", "attention", "attention_update") else 256
-    if a.case in ("layer", "attention", "attention_update"):
+        a.k = 308 if a.case in rows else 256
+    if a.kv8_block is None:
+        a.kv8_block = 0 if a.case.startswith("step") else 64
+    if a.case in rows:
         a.N = 1536 if a.N == 12288 else a.N
     out = {"gemm": case_gemm, "score": case_score, "layer": case_layer,
            "attention": case_attention, "attention_update": case_attention_update,
-           "step": case_step, "step_graph": case_step_graph}[a.case](a)
+           "attention_kv8": case_attention_kv8, "write_kv8": case_write_kv8,
+           "read_kv8": case_read_kv8, "qk_norm": case_qk_norm, "step": case_step,
+           "step_graph": case_step_graph}[a.case](a)
     print(json.dumps(out))
 
 
