@@ -52,9 +52,9 @@ def test_only_blocks_of_zeros(lib, rows):
 
 # ------------------------------------------------------------------ weights
 
-def weight_bound(q, K, V, vs):
+def weight_bound(q, K, V, vs, width):
     """One head: the output [R, hd] of q [R, hd] over K, V [n, hd] (vs [n]: V's scales) and a bound
-    of its error before the store.  Weights come in tiles of 64 keys (16 where few rows ask).  With
+    of its error before the store.  Weights come in tiles of `width` keys.  With
     the largest weight * scale of a tile brought to 2^-6 or more, f16 holds the others to half a
     step, 2^-11 of each, or to 2^-25 where they are below 2^-14: 2^-25 / 2^-6 = 2^-19 of the largest.
     Where a tile's scales span more than six octaves its codes are first brought towards a common
@@ -67,11 +67,11 @@ def weight_bound(q, K, V, vs):
     mag = np.abs(q) @ np.abs(K).T / math.sqrt(hd)
     ds = ((hd / 16 + 2) * 2.0 ** -23 * mag + 2.0 ** -22 * np.abs(s)).max(1, keepdims=True)
     tol = (2.0 ** -11 + 2 * ds + n / 16 * 2.0 ** -23 + 2.0 ** -20) * (p @ np.abs(V))
-    for t in range(0, n, 64):
-        e = np.log2(vs[t:t + 64])
+    for t in range(0, n, width):
+        e = np.log2(vs[t:t + width])
         mixed = e.max() - e.min() > 6
         unit = 2.0 ** (e - np.clip(e - e.max() + 1, -7, 1)) if mixed else 2.0 ** e
-        tol += 2.0 ** (-33 if mixed else -19) * (p[:, t:t + 64] * unit).max(1, keepdims=True) * (np.abs(V[t:t + 64]) / unit[:, None]).sum(0)
+        tol += 2.0 ** (-33 if mixed else -19) * (p[:, t:t + width] * unit).max(1, keepdims=True) * (np.abs(V[t:t + width]) / unit[:, None]).sum(0)
     return p @ V / l, tol / l, p @ np.abs(V) / l
 
 
@@ -87,7 +87,8 @@ def check_weights(lib, q, cache, block, rows, where, tight=True):
     for b, h in where:
         one = lambda c, sc: decoded(c[b:b + 1, :, h:h + 1], sc[b:b + 1, h:h + 1], block)[0, :, 0]
         at = lambda t: f64(t.view(B, rows, H, hd)[b, :, h])
-        ref, tol, size = weight_bound(at(q), one(k8, ks), one(v8, vs), f64(vs[b, h]).repeat(block)[:N])
+        ref, tol, size = weight_bound(at(q), one(k8, ks), one(v8, vs), f64(vs[b, h]).repeat(block)[:N],
+                                      64 if rows > 16 else 16)   # (few rows: tiles of 16 keys)
         assert not tight or np.all(tol <= 2.0 ** -9 * size)
         err = np.abs(at(o) - ref) - (tol + 2.0 ** -8 * (np.abs(ref) + tol))
         assert np.all(err <= 0), (b, h, err.max())
