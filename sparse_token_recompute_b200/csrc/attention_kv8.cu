@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(RW * 32, 4)
           for (int y = 0; y < L::VB / 4; ++y)
             if (v_key[x] >= left) w[x][y] = 0;
       }
-      float top[2], f[2], alpha[2] = {1.f, 1.f};
+      float top[2], f[2];
       bool move[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -317,12 +317,15 @@ __global__ void __launch_bounds__(RW * 32, 4)
         f[x] = fc[x] * inv_v;  // 0: far
       }
       if (__any_sync(0xffffffffu, move[0] || move[1] || f[0] == 0.f || f[1] == 0.f)) {
+        float rise[2];
+        bool twice = false;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[x] *= k[x];
           const float before = m[x];
           move[x] = new_ref(top[x] + ev, m[x], low[x]);
-          if (move[x]) alpha[x] = exp2_approx(before - m[x]);
+          rise[x] = before - m[x];
+          twice |= rises_far(before, m[x]);
           if (top[x] > lm[x] && (move[x] || f[x] == 0.f)) {
             l[x] *= exp2_approx(lm[x] - top[x]);
             lm[x] = top[x];
@@ -337,9 +340,13 @@ __global__ void __launch_bounds__(RW * 32, 4)
             }
           }
         }
+        twice = __any_sync(0xffffffffu, twice);
+        const float a0 = exp2_approx(twice ? 0.5f * rise[0] : rise[0]), a1 = exp2_approx(twice ? 0.5f * rise[1] : rise[1]);
+#pragma unroll 1
+        for (int i = twice ? 0 : 1; i < 2; ++i) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          o[n][0] *= alpha[0], o[n][1] *= alpha[0], o[n][2] *= alpha[1], o[n][3] *= alpha[1];
+          for (int n = 0; n < NT; ++n) o[n][0] *= a0, o[n][1] *= a0, o[n][2] *= a1, o[n][3] *= a1;
+        }
       }
       float p[2][4];
 #pragma unroll

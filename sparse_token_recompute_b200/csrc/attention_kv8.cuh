@@ -81,6 +81,11 @@ __device__ __forceinline__ bool new_ref(float mx, float& m, float& low, bool mix
   low = fmaxf(low, m - kKv8Fall);
   return true;
 }
+// A rise after a fall may pass 2^126, where O's factor would flush to zero: O is multiplied
+// twice then (not at the first reference, where O is zero)
+__device__ __forceinline__ bool rises_far(float before, float after) {
+  return before - after < -120.f && before > kKv8NoRef;
+}
 // 2^(weights' reference - sum's reference), 0 if that is far above 1
 __device__ __forceinline__ float ref_factor(float d) { return d <= (float)kKv8Far ? exp2_approx(d) : 0.f; }
 // (m, l) with the same l 2^m and 1 <= l < 2; l = 0 stays, with m = -inf

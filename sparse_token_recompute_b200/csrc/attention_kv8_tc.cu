@@ -456,36 +456,38 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args 
           if (__any_sync(0xffffffffu, wants_ref(mx - m, mixed))) {
             const float before = m;
             const bool move = new_ref(mx, m, low, mixed);
-            const float alpha = move ? exp2_approx(before - m) : 1.f;  // the first time: 0
             if (move) raise_sum(sc[0].z != 0.f ? m - sc[0].y : lm);
             if (j > 0 && __any_sync(0xffffffffu, move)) {
               // O may be rescaled once PV(j-1) is complete, until P(j) is handed over
               if (!__all_sync(0xffffffffu, mbar_wait(pv_done(j - 1), par(j - 1), abort_flag, status)))
                 return false;
               tc_fence_after();
-              if constexpr (HD == 128) {  // in the scores' registers, which are read again
+              const bool twice = __any_sync(0xffffffffu, rises_far(before, m));
+              const float alpha = exp2_approx(twice ? 0.5f * (before - m) : before - m);
 #pragma unroll 1
-                for (int c = 0; c < HD; c += 64) {
-                  tmem_ld32_nowait(tO + lane_off + c, s);
-                  tmem_ld32_nowait(tO + lane_off + c + 32, s + 32);
+              for (int c = twice ? 0 : HD; c < 2 * HD; c += HD == 128 ? 64 : 16) {
+                const uint32_t at = tO + lane_off + c % HD;
+                if (c == HD && twice) tmem_wait_st();  // (the second turn reads the first's)
+                if constexpr (HD == 128) {  // in the scores' registers, which are read again
+                  tmem_ld32_nowait(at, s);
+                  tmem_ld32_nowait(at + 32, s + 32);
                   tmem_wait_ld();
 #pragma unroll
                   for (int i = 0; i < 64; ++i) s[i] *= alpha;
-                  tmem_st32(tO + lane_off + c, reinterpret_cast<const uint32_t*>(s));
-                  tmem_st32(tO + lane_off + c + 32, reinterpret_cast<const uint32_t*>(s) + 32);
+                  tmem_st32(at, reinterpret_cast<const uint32_t*>(s));
+                  tmem_st32(at + 32, reinterpret_cast<const uint32_t*>(s) + 32);
+                } else {
+                  float o[16];
+                  tmem_ld16(at, o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                  tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
                 }
+              }
+              if constexpr (HD == 128) {
                 tmem_ld32_nowait(tS(j) + lane_off, s);
                 tmem_ld32_nowait(tS(j) + lane_off + 32, s + 32);
                 tmem_wait_ld();
-              } else {
-#pragma unroll 1
-                for (int c = 0; c < HD; c += 16) {
-                  float o[16];
-                  tmem_ld16(tO + lane_off + c, o);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                  tmem_st16(tO + lane_off + c, reinterpret_cast<const uint32_t*>(o));
-                }
               }
             }
           }

@@ -194,6 +194,29 @@ def test_heavy_keys_of_a_small_block_beside_light_ones_of_a_large(lib, rows, apa
                   apart <= 30)   # (60: the small block's products are 2^-40 of the largest)
 
 
+@pytest.mark.parametrize("rows", [1, 130])
+@pytest.mark.parametrize("scales", [(48, -31, 109), (0, -62, 62), (0, -40, -62, 65, -10, 60)])
+def test_scales_that_fall_far_and_rise_further(lib, rows, scales):
+    """Blocks of a tile each, alone in their channels: the weights' reference falls by up to 2^64
+    and rises by more than 2^126 at once; what was summed before keeps its bits."""
+    hd, block = 128, 64
+    N = block * len(scales)
+    k8, ks, v8, vs = lib.kv8_cache(1, N, 1, hd, block)
+    k8.copy_((normal((1, N, 1, hd), 1) * 100).clamp(-448, 448).to(torch.float8_e4m3fn))
+    ks.fill_(2.0 ** -7)
+    code = torch.zeros(1, N, 1, hd, device="cuda")
+    for i in range(len(scales)):
+        code[0, i * block:(i + 1) * block, 0, i * 20:(i + 1) * 20] = 100 * normal((block, 20), 5 + i)
+    v8.copy_(code.clamp(-448, 448).to(torch.float8_e4m3fn))
+    vs.copy_(torch.exp2(torch.tensor(scales, device="cuda").float()).expand_as(vs))
+    # (products 2^83 below the largest are past what the weights hold)
+    live = [i for i, e in enumerate(scales) if e > max(scales) - 75]
+    assert len(live) >= 2
+    v8.view(torch.uint8)[:, [n for n in range(N) if n // block not in live]] = 0
+    q = normal((UNITS[0] * rows, UNITS[1] * hd), 3) * 0.1
+    check_weights(lib, q.to(BF), many((k8, ks, v8, vs)), block, rows, WHERE)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 40])
 @pytest.mark.parametrize("N", [100, 1000, 9000])
 def test_values_at_the_end_of_the_range(lib, rows, N):
