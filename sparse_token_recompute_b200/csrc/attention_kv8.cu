@@ -84,8 +84,8 @@ struct RowsSmem {
 // order of the inner index that Q's fragments share; V by gathering one byte of two
 // keys.  With so few rows the tensor cores' rate does not matter and the kernel is
 // bound by the codes' way: 2 bytes per key and head_dim element.  32 sequences x 1 row x
-// 1536 keys, 32 heads of 128 over 32 (403 MB): 75 us, 5.4 TB/s; 1 x 1 x 16384 keys (134
-// MB) 32 us, start-up and merge included.
+// 1536 keys, 32 heads of 128 over 32 (403 MB): 76 us, 5.3 TB/s; 1 x 1 x 16384 keys (134
+// MB) 33 us, start-up and merge included.
 template <int HD>
 __global__ void __launch_bounds__(RW * 32, 4)
     attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,

@@ -20,9 +20,9 @@
 //
 // Bound by shared memory: per 64 keys a CTA moves 128 KB through it (codes in and
 // out 32, f16 tiles 32, Q and K for Q K^T 48, V 16) = 1024 cycles at 128 bytes a
-// cycle.  32 sequences x 308 rows x 1536 keys, 32 heads of 128: over 8 kv heads 346 us
-// (716 TFLOP/s; the kernel over a bf16 cache 346), over 32, where the third of each
-// sequence's tiles holds 52 of 128 rows, 401 (358); under the power cap, at 1.78 GHz, 445.
+// cycle.  32 sequences x 308 rows x 1536 keys, 32 heads of 128: over 8 kv heads 347 us
+// (714 TFLOP/s; the kernel over a bf16 cache 347), over 32, where the third of each
+// sequence's tiles holds 52 of 128 rows, 402 (358); under the power cap, at 1.78 GHz, 446.
 // Dropped on the way, at the latter: scores read twice and 128 keys 696 us; codes through
 // registers and L1 540; K and V converted in turn by the same warps 445.  Two row tiles per
 // CTA over the same keys, one CTA per SM, 378 us at 256 rows against 350; codes by TMA 468
@@ -69,8 +69,8 @@ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// MIX: blocks shorter than a tile of keys, whose V scales may differ within it (407 us where
-// blocks of 64 take 401)
+// MIX: blocks shorter than a tile of keys, whose V scales may differ within it (413 us where
+// blocks of 64 take 402)
 template <int HD, bool MIX>
 __global__ void __launch_bounds__(kThreads, 2) attn_kv8_tc_kernel(const Kv8Args A) {
   using L = Smem<HD>;

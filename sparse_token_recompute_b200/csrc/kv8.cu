@@ -78,11 +78,10 @@ struct NormRows {
 // keys) are spread over `lanes` threads, each with PASSES of them; a thread takes
 // `rows` rows one after the other, the next one's vectors on their way while it
 // works on the current.  The sums, the norm and the rotation are fp32, rounded once
-// when stored.  Bound by HBM, closely followed by instruction issue: hence addresses
-// that are set up once per thread, and gains in shared memory as bf16 (fp32 there, with
-// twice the reads: 66 us; in registers, at the cost of a CTA per SM: 75).  32 sequences x
-// up to 308 rows of 32 + 32 heads of 128 (279 MB): 64 us, 4.4 TB/s; a copy of the same
-// rows in this shape takes 60.
+// when stored.  Bound by HBM, closely followed by instruction issue (66 % active): hence
+// addresses that are set up once per thread, and gains in shared memory as bf16 (fp32
+// there, with twice the reads: 66 us; in registers, at the cost of a CTA per SM: 75).  32
+// sequences x up to 308 rows of 32 + 32 heads of 128 (279 MB): 62.6 us, 4.5 TB/s.
 template <int HD, int PASSES>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const NormArgs A, int lanes, int rows) {
   griddep_launch_dependents();
@@ -265,9 +264,9 @@ __device__ __forceinline__ int warp_lower_bound(const int* __restrict__ l, int n
 // time, as many as hold its new rows in registers: largest magnitude, the block's
 // scale, encode and store.  Tokens that are kept are read only where the scale grew.
 // Few rows are bound by the way list -> rows -> scale -> kept codes, each a trip to
-// memory, and by instruction issue (74 % active); many by HBM.  32 sequences, 32 heads of
-// 128, blocks of 64: up to 308 of 1536 rows (206 MB) 48 us, 4.3 TB/s; all rows (1.2 GB)
-// 200 us, 6.0 TB/s (before, one warp with a second look at the rows: 234).  Four CTAs per
+// memory, and by instruction issue (78 % active); many by HBM.  32 sequences, 32 heads of
+// 128, blocks of 64: up to 308 of 1536 rows (206 MB) 47 us, 4.4 TB/s; all rows (1.2 GB)
+// 202 us, 6.0 TB/s (before, one warp with a second look at the rows: 234).  Four CTAs per
 // SM 50 and 201 us, six 52 and 222.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 5) kv8_write_kernel(const WriteArgs A) {
@@ -470,7 +469,7 @@ struct ReadArgs {
 // `lanes` threads per row, 16 codes of K and of V per thread and turn; several rows one
 // after the other, so that the addresses of a row cost little: what is fixed for a
 // thread is its place in the row.  Bound by HBM (a third read, two thirds written): 32 x
-// 1536 rows of 32 heads of 128 (1.2 GB) 200 us, 6.0 TB/s.
+// 1536 rows of 32 heads of 128 (1.2 GB) 202 us, 6.0 TB/s.
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const ReadArgs A, int lanes, int rows) {
   griddep_launch_dependents();
   griddep_wait();
